@@ -475,6 +475,71 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
                                                 size_t workspace_bytes, bitnet_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Softmax cross entropy of an output head over its whole vocabulary, with
+ * its gradient, without keeping the logits.  The head of a fine-tuned model
+ * stays in 16 bits (the first page quantizes the linear layers of the blocks
+ * only), so this is the loss that the warm-up's training step starts from.
+ *   z = x W^T;  lse_m = log sum_v exp(z_mv);  loss_m = lse_m - z_m,targets[m]
+ *   g_mv = dloss_m (exp(z_mv - lse_m) - [v = targets[m]]);  dx = g W;  dW = g^T x
+ * A target outside [0, V) (the usual -100, say) marks a token without loss:
+ * loss_m = 0 and the row of g is 0 whatever x holds; lse_m is still written.
+ *
+ *   x [M][K], W [V][K] bf16; targets [M] int64; loss, lse, dloss [M] fp32;
+ *   dx [M][K], dW [V][K] bf16, either may be NULL (not computed).
+ *   All sums and the softmax's maximum, sum and logarithm are fp32; g is
+ *   rounded to bf16 as an operand of the two gradient products.
+ *   Non-finite logits of a row give a non-finite or NaN lse and loss.
+ *   M == 0: the forward queues nothing, the backward zeroes dW.
+ * Shapes: K % 8 == 0, 8 <= K <= BITNET_MAX_K, 1 <= V <= BITNET_MAX_N,
+ * M <= BITNET_MAX_M, ceil(M/128) * ceil(V/128) <= 2^30; else
+ * BITNET_ERR_UNSUPPORTED_SHAPE (and a workspace size of 0).
+ * x, W, dx, dW 16-byte aligned, targets 8, the rest 4; workspace >= the size
+ * query, 256-byte aligned, contents on entry irrelevant; one per call in
+ * flight.  The backward takes lse as the forward wrote it.
+ * The same inputs give the same bits on every call.
+ * ---------------------------------------------------------------------- */
+BITNET_API size_t bitnet_cross_entropy_forward_workspace_bytes(int64_t M, int64_t V, int64_t K);
+BITNET_API bitnet_status bitnet_cross_entropy_forward(const void *x, const void *W,
+                                                      const int64_t *targets, int64_t M,
+                                                      int64_t V, int64_t K, float *loss,
+                                                      float *lse, void *workspace,
+                                                      size_t workspace_bytes,
+                                                      bitnet_stream_t stream);
+BITNET_API size_t bitnet_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
+BITNET_API bitnet_status bitnet_cross_entropy_backward(const void *x, const void *W,
+                                                       const int64_t *targets, const float *lse,
+                                                       const float *dloss, int64_t M, int64_t V,
+                                                       int64_t K, void *dx, void *dW,
+                                                       void *workspace, size_t workspace_bytes,
+                                                       bitnet_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bitnet_orthogonalize -- the orthogonalised update of a weight matrix by
+ * Newton-Schulz products: what an optimiser applies to a layer's latent
+ * weights in place of their averaged gradient (bitnet_warmup_backward's dW).
+ *   X = U / (||U||_F + eps), transposed when N > K
+ *   `steps` times: A = X X^T, X <- a X + (b A + c A A) X;   O = X, transposed back
+ *
+ *   U            [B][N][K] fp32 or bf16 (u_dtype): B matrices, each on its own.
+ *   coefficients host array of 3 * steps doubles: a, b, c of each step.
+ *   O            [B][N][K] bf16 out; must not overlap U.
+ *   X is held in 22 bits, A's and b A + c A A's diagonals in fp32, sums in
+ *   fp32; the products' operands are fp16.  A non-finite entry makes its
+ *   matrix NaN, a zero matrix gives zeros (eps 0 included).
+ * 1 <= steps <= 32, eps >= 0; the coefficients finite and such that no step
+ * takes singular values of at most 1 beyond 2^20 (BITNET_ERR_INVALID_ARG).
+ * Shapes: 1 <= N, K <= BITNET_MAX_K, 0 <= B <= 65535, at most 2^30 tiles of
+ * 128 x 128 in all.  U, O 16-byte aligned; workspace >= the size query,
+ * 256-byte aligned, contents on entry irrelevant; one per call in flight.
+ * The same input gives the same bits on every call.
+ * ---------------------------------------------------------------------- */
+BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K);
+BITNET_API bitnet_status bitnet_orthogonalize(const void *U, int u_dtype, int64_t B, int64_t N,
+                                              int64_t K, int steps, const double *coefficients,
+                                              float eps, void *O, void *workspace,
+                                              size_t workspace_bytes, bitnet_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * BitDelta ("【論文要約】BitDelta: Your Fine-Tune May Only Be Worth One Bit",
  * Eq. 1-4: Delta = W_fine - W_base is stored as its sign and one scale per
  * matrix, alpha = mean |Delta|; Eq. 6 and Fig. 4: a shared base matrix

@@ -8,6 +8,7 @@ CUDA kernels; PyTorch only provides device memory and streams.  There is no
 CPU fallback: if the library is missing or a call fails, an exception is
 raised.
 """
+import contextlib
 import ctypes
 import os
 import threading
@@ -61,6 +62,9 @@ EXPORTED = (
     "bitnet_warmup_backward_workspace_bytes", "bitnet_warmup_backward",
     "bitnet_bitdelta_compress_workspace_bytes", "bitnet_bitdelta_compress",
     "bitnet_bitdelta_forward",
+    "bitnet_cross_entropy_forward_workspace_bytes", "bitnet_cross_entropy_forward",
+    "bitnet_cross_entropy_backward_workspace_bytes", "bitnet_cross_entropy_backward",
+    "bitnet_orthogonalize_workspace_bytes", "bitnet_orthogonalize",
 )
 
 BITNET_LAYOUT_ROWS = 0
@@ -148,6 +152,13 @@ def load_library(path: str = LIB_PATH):
             "bitnet_bitdelta_compress_workspace_bytes": ([I64, I64], SZ),
             "bitnet_bitdelta_compress": ([P, P, I64, I64, P, P, P, SZ, P], I),
             "bitnet_bitdelta_forward": ([P, P, P, P, I64, I64, I64, P, I, P], I),
+            "bitnet_cross_entropy_forward_workspace_bytes": ([I64, I64, I64], SZ),
+            "bitnet_cross_entropy_forward": ([P, P, P, I64, I64, I64, P, P, P, SZ, P], I),
+            "bitnet_cross_entropy_backward_workspace_bytes": ([I64, I64, I64], SZ),
+            "bitnet_cross_entropy_backward": (
+                [P, P, P, P, P, I64, I64, I64, P, P, P, SZ, P], I),
+            "bitnet_orthogonalize_workspace_bytes": ([I64, I64, I64], SZ),
+            "bitnet_orthogonalize": ([P, I, I64, I64, I64, I, P, F, P, P, SZ, P], I),
         }
         for name, (argtypes, restype) in sig.items():
             fn = getattr(lib, name)
@@ -714,6 +725,147 @@ def bitnet_bitdelta_forward(x, W_base, signs, alpha, y_dtype=torch.float32, y=No
         _ptr(x), _ptr(W_base), _ptr(signs), _ptr(alpha), B, N, K, _ptr(y),
         _dtype_code(y.dtype), _stream(stream)))
     return y
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Run on `device` and on `stream` (the device's current one when None):
+    memory allocated inside belongs to the stream the kernels run on, so a
+    buffer freed on return is not handed to another stream's work."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _same_device(first, *ts):
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors must be on one device, got {first.device} and {t.device}")
+
+
+def _scratch(workspace, nbytes, device):
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device) \
+        if workspace is None else workspace
+
+
+def _expect_head(x, W, targets):
+    _expect(x, "x", torch.bfloat16)
+    _expect(W, "W", torch.bfloat16)
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError("x must be [M, K] and W [V, K]")
+    M, K = x.shape
+    _expect(targets, "targets", torch.int64, shape=(M,))
+    if K < 8 or K % 8:
+        raise ValueError(f"K must be a multiple of 8, got {K}")
+    return M, W.shape[0], K
+
+
+def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=None, stream=None):
+    """Cross entropy of an output head, without keeping the logits x W^T:
+    x bf16 [M,K], W bf16 [V,K], targets int64 [M] -> (loss fp32 [M], lse fp32
+    [M]), loss = lse - logit of the target.  A target outside [0, V) marks a
+    token without loss (0).  lse goes to bitnet_cross_entropy_backward."""
+    M, V, K = _expect_head(x, W, targets)
+    for t, name in ((loss, "loss"), (lse, "lse")):
+        if t is not None:
+            _expect(t, name, torch.float32, shape=(M,))
+    lib = load_library()
+    nb = int(lib.bitnet_cross_entropy_forward_workspace_bytes(M, V, K))
+    if workspace is not None:
+        _expect(workspace, "workspace", torch.uint8, numel=nb)
+    _need_cuda(x, W, targets, loss, lse, workspace)
+    _same_device(x, W, targets, loss, lse, workspace)
+    with _on(x.device, stream):
+        if loss is None:
+            loss = torch.empty((M,), dtype=torch.float32, device=x.device)
+        if lse is None:
+            lse = torch.empty((M,), dtype=torch.float32, device=x.device)
+        ws = _scratch(workspace, nb, x.device)
+        _check("bitnet_cross_entropy_forward", lib.bitnet_cross_entropy_forward(
+            _ptr(x), _ptr(W), _ptr(targets), M, V, K, _ptr(loss), _ptr(lse), _ptr(ws),
+            ws.numel(), _stream()))
+    return loss, lse
+
+
+def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_dW=True, dx=None,
+                                  dW=None, workspace=None, stream=None):
+    """Gradient of sum(dloss * loss) of bitnet_cross_entropy_forward: (dx bf16
+    [M,K], dW bf16 [V,K]); either may be skipped (None).  dloss fp32 [M] is
+    the gradient of each token's loss (for a mean, 1 / count each); the logits
+    are computed again, a piece of the vocabulary at a time."""
+    M, V, K = _expect_head(x, W, targets)
+    _expect(lse, "lse", torch.float32, shape=(M,))
+    _expect(dloss, "dloss", torch.float32, shape=(M,))
+    if dx is not None:
+        _expect(dx, "dx", torch.bfloat16, shape=(M, K))
+    if dW is not None:
+        _expect(dW, "dW", torch.bfloat16, shape=(V, K))
+    lib = load_library()
+    nb = int(lib.bitnet_cross_entropy_backward_workspace_bytes(M, V, K))
+    if workspace is not None:
+        _expect(workspace, "workspace", torch.uint8, numel=nb)
+    _need_cuda(x, W, targets, lse, dloss, dx, dW, workspace)
+    _same_device(x, W, targets, lse, dloss, dx, dW, workspace)
+    with _on(x.device, stream):
+        if dx is None and need_dx:
+            dx = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        if dW is None and need_dW:
+            dW = torch.empty((V, K), dtype=torch.bfloat16, device=x.device)
+        dx, dW = dx if need_dx else None, dW if need_dW else None
+        ws = _scratch(workspace, nb, x.device)
+        _check("bitnet_cross_entropy_backward", lib.bitnet_cross_entropy_backward(
+            _ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K, _ptr(dx), _ptr(dW),
+            _ptr(ws), ws.numel(), _stream()))
+    return dx, dW
+
+
+# Coefficients a, b, c of the quintic step that bitnet_orthogonalize takes by
+# default: singular values end between about 0.7 and 1.2 after five steps.
+ORTHOGONALIZE_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def bitnet_orthogonalize(U, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7, out=None,
+                         workspace=None, stream=None):
+    """Newton-Schulz orthogonalisation of an update: U fp32 or bf16 [N,K], or
+    [B,N,K] for B matrices, -> bf16 of U's shape.  X = U / (|U|_F + eps), then
+    `steps` times X <- a X + (b A + c A A) X with A = X X^T (on the smaller
+    side).  coefficients: (a, b, c), or one such triple for each step."""
+    _expect(U, "U", (torch.float32, torch.bfloat16))
+    if U.dim() not in (2, 3):
+        raise ValueError("U must be [N, K] or [B, N, K]")
+    B = U.shape[0] if U.dim() == 3 else 1
+    N, K = U.shape[-2:]
+    steps = int(steps)
+    if not 1 <= steps <= 32:
+        raise ValueError(f"steps must be between 1 and 32, got {steps}")
+    rows = list(coefficients)
+    if len(rows) == 3 and all(isinstance(c, (int, float)) for c in rows):
+        rows = [rows] * steps
+    flat = [float(c) for row in rows for c in row]
+    if len(rows) != steps or len(flat) != 3 * steps or any(len(row) != 3 for row in rows):
+        raise ValueError("coefficients must be (a, b, c), or one such triple for each step")
+    if out is not None:
+        _expect(out, "out", torch.bfloat16, shape=tuple(U.shape))
+    lib = load_library()
+    nb = int(lib.bitnet_orthogonalize_workspace_bytes(B, N, K))
+    if workspace is not None:
+        _expect(workspace, "workspace", torch.uint8, numel=nb)
+    _need_cuda(U, out, workspace)
+    _same_device(U, out, workspace)
+    with _on(U.device, stream):
+        if out is None:
+            out = torch.empty(tuple(U.shape), dtype=torch.bfloat16, device=U.device)
+        ws = _scratch(workspace, nb, U.device)
+        _check("bitnet_orthogonalize", lib.bitnet_orthogonalize(
+            _ptr(U), _dtype_code(U.dtype), B, N, K, steps,
+            (ctypes.c_double * (3 * steps))(*flat), ctypes.c_float(eps), _ptr(out), _ptr(ws),
+            ws.numel(), _stream()))
+    return out
 
 
 def _weights_ptr_layout(W, K):

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -18,11 +19,14 @@
 #include "act_quant.cuh"
 #include "bitdelta.cuh"
 #include "common.cuh"
+#include "cross_entropy.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
 #include "gemv_tiled.cuh"
 #include "group_quant.cuh"
+#include "orthogonalize.cuh"
 #include "peak.cuh"
+#include "tc_gemm.cuh"
 #include "tiled.cuh"
 #include "warmup.cuh"
 #include "weight_quant.cuh"
@@ -2088,3 +2092,5 @@ extern "C" BITNET_API bitnet_status bitnet_quantize_pack_weights_static(
       W, nwords, s_w, reinterpret_cast<uint32_t*>(W_packed));
   return launch_status();
 }
+
+#include "training_capi.cuh"

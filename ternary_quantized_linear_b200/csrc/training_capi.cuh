@@ -1,0 +1,625 @@
+// training_capi.cuh -- host side of the training operators (vocabulary cross
+// entropy, orthogonalised updates): argument checks, workspace layouts,
+// launch planning and the C entry points.  Included by bitnet_capi.cu, whose
+// helpers it uses.
+#pragma once
+
+namespace bitnet {
+namespace {
+
+// The SM count that plans and workspace sizes assume (size queries run
+// without a device).  A device with another count gets the same results.
+constexpr int kPlanSms = 148;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// ------------------------------------------------------------ matrix product
+
+// One operand: `rows` (m or n) x contraction, K-major (k contiguous) or
+// MN-major, row stride ld and batch stride in elements.
+struct TgOperand {
+  const void* p = nullptr;
+  const void* lo = nullptr;
+  int64_t ld = 0, batch_stride = 0;
+  bool mn = false;
+};
+
+struct TgProblem {
+  TgOperand a, b;
+  int64_t M = 0, N = 0, Kc = 0, batch = 1;
+  bool bf16 = true;
+  bool sym = false;
+  int passes = 1;
+  int ksplit = 1;
+};
+
+// 3-D tensor [batch][rows][inner] of 16-bit elements, boxes of 64 x box_rows,
+// 128-byte swizzle; out-of-range elements read as zero.
+bool make_tmap_16(CUtensorMap* map, const void* base, bool bf16, int64_t inner, int64_t rows,
+                  int64_t batch, int64_t ld, int64_t batch_stride, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(batch)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * ld),
+                           static_cast<cuuint64_t>(2 * (batch > 1 ? batch_stride : ld * rows))};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_operand_map(CUtensorMap* map, const TgOperand& o, const void* base, bool bf16,
+                      int64_t rows, int64_t Kc, int64_t batch, int tile_rows) {
+  return o.mn ? make_tmap_16(map, base, bf16, rows, Kc, batch, o.ld, o.batch_stride, 64)
+              : make_tmap_16(map, base, bf16, Kc, rows, batch, o.ld, o.batch_stride, tile_rows);
+}
+
+int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) {
+  const int64_t mt = ceil_div(M, bm), nt = ceil_div(N, bn);
+  return batch * (sym ? mt * (mt + 1) / 2 : mt * nt);
+}
+
+// Whether a product takes 256 x 256 tiles on SM pairs rather than 128 x 128
+// tiles: whichever needs less time for its waves of tiles, a 256-tile's step
+// costing a pair twice a 128-tile's step on one SM, and the small tile's
+// step, which reads twice the shared memory per MMA, 1.3 times its share.
+bool tg_use_pairs(int64_t M, int64_t N, int64_t batch, bool sym) {
+  const int64_t t2 = tg_tiles(M, N, batch, sym, 256, 256);
+  const int64_t t1 = tg_tiles(M, N, batch, sym, 128, 128);
+  return 2.0 * static_cast<double>(ceil_div(t2, kPlanSms / 2)) <
+         1.3 * static_cast<double>(ceil_div(t1, kPlanSms));
+}
+
+// Resident workers (pairs or single CTAs) of one kernel instance, per device;
+// sets the kernel's shared-memory limit the first time.
+template <int CG, int BN, class Epi>
+int tg_workers(int num_sms) {
+  static std::once_flag once[kMaxDevices];
+  static int workers[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::call_once(once[dev], [dev, num_sms]() {
+    using C = TgCfg<CG, BN>;
+    auto kernel = tc_gemm_kernel<CG, BN, Epi>;
+    if (!set_smem(kernel, C::SMEM_DYN)) return;
+    if (CG == 1) {
+      workers[dev] = num_sms;
+      return;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
+    cfg.blockDim = dim3(kTgThreads);
+    cfg.dynamicSmemBytes = C::SMEM_DYN;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) workers[dev] = n;
+  });
+  return workers[dev];
+}
+
+template <int CG, int BN, class Epi>
+bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
+                            const typename Epi::Params& ep, cudaStream_t stream) {
+  using C = TgCfg<CG, BN>;
+  const int workers = tg_workers<CG, BN, Epi>(ds.num_sms);
+  if (workers < 1) return cuda_status(cudaErrorInvalidConfiguration);
+  TgMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!make_operand_map(&maps.a, g.a, g.a.p, g.bf16, g.M, g.Kc, g.batch, 128) ||
+      !make_operand_map(&maps.b, g.b, g.b.p, g.bf16, g.N, g.Kc, g.batch, C::B_ROWS))
+    return BITNET_ERR_CUDA;
+  if (g.passes == 3 &&
+      (!make_operand_map(&maps.a_lo, g.a, g.a.lo, g.bf16, g.M, g.Kc, g.batch, 128) ||
+       !make_operand_map(&maps.b_lo, g.b, g.b.lo, g.bf16, g.N, g.Kc, g.batch, C::B_ROWS)))
+    return BITNET_ERR_CUDA;
+  TgShape p{};
+  p.M = static_cast<int>(g.M);
+  p.N = static_cast<int>(g.N);
+  p.steps = static_cast<int>(ceil_div(g.Kc, kTgKStep));
+  p.mt = static_cast<int>(ceil_div(g.M, 128 * CG));
+  p.nt = static_cast<int>(ceil_div(g.N, BN));
+  p.sym = g.sym ? 1 : 0;
+  p.per_batch = static_cast<int>(tg_tiles(g.M, g.N, 1, g.sym, 128 * CG, BN));
+  p.split_steps = static_cast<int>(ceil_div(p.steps, g.ksplit));
+  p.ksplit = g.ksplit;
+  p.tiles = static_cast<int>(g.batch * p.per_batch * p.ksplit);
+  p.group = 8;
+  p.passes = g.passes;
+  p.a_mn = g.a.mn ? 1 : 0;
+  p.b_mn = g.b.mn ? 1 : 0;
+  p.idesc = tg_idesc(128 * CG, BN, g.bf16, g.a.mn, g.b.mn);
+  p.status = ds.status;
+  p.wait_limit_ns = kWaitLimitNs;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(CG * std::min(workers, p.tiles)));
+  cfg.blockDim = dim3(kTgThreads);
+  cfg.dynamicSmemBytes = C::SMEM_DYN;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, tc_gemm_kernel<CG, BN, Epi>, maps, p, ep));
+}
+
+template <class Epi>
+bitnet_status launch_tg(const DeviceState& ds, const TgProblem& g, bool pairs,
+                        const typename Epi::Params& ep, cudaStream_t stream) {
+  return pairs ? launch_tg_cfg<2, 256, Epi>(ds, g, ep, stream)
+               : launch_tg_cfg<1, 128, Epi>(ds, g, ep, stream);
+}
+
+template <typename... KArgs, typename... Args>
+bitnet_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned threads,
+                         cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...));
+}
+
+// ------------------------------------------------------------- cross entropy
+
+// Limits: as the warm-up's, and tile indices in 32 bits.
+bitnet_status check_ce_shape(int64_t M, int64_t V, int64_t K) {
+  if (M < 0 || V < 0 || K < 0) return BITNET_ERR_INVALID_ARG;
+  if (V < 1 || V > BITNET_MAX_N || K < 8 || K % 8 != 0 || K > BITNET_MAX_K || M > BITNET_MAX_M ||
+      ceil_div(M, 128) * ceil_div(V, 128) > (1LL << 30))
+    return BITNET_ERR_UNSUPPORTED_SHAPE;
+  return BITNET_OK;
+}
+
+struct CeFwdLayout {
+  bool pairs;
+  int64_t parts;
+  size_t part, logit, total;
+};
+
+CeFwdLayout ce_fwd_layout(int64_t M, int64_t V) {
+  CeFwdLayout w{};
+  w.pairs = tg_use_pairs(M, V, 1, false);
+  w.parts = 2 * ceil_div(V, w.pairs ? 256 : 128);
+  size_t o = 0;
+  w.part = o;
+  o = align256(o + static_cast<size_t>(8 * w.parts * M));
+  w.logit = o;
+  o = align256(o + static_cast<size_t>(4 * M));
+  w.total = o;
+  return w;
+}
+
+// Bytes of g that one piece of the vocabulary may take.
+constexpr int64_t kCePieceBytes = 256LL << 20;
+
+struct CeBwdLayout {
+  int64_t cols, pieces;      // vocabulary columns of a piece, number of pieces
+  bool dx_pairs;
+  int dx_split;
+  size_t g, acc, part, scale, total;
+};
+
+CeBwdLayout ce_bwd_layout(int64_t M, int64_t V, int64_t K) {
+  CeBwdLayout w{};
+  const int64_t most = std::max<int64_t>(256, kCePieceBytes / (2 * M) / 256 * 256);
+  w.pieces = ceil_div(V, most);
+  w.cols = round_up(ceil_div(V, w.pieces), 256);
+  w.pieces = ceil_div(V, w.cols);
+  // dx has few tiles and a long contraction: split it so that the last wave
+  // of tiles is full (at most 16 slices, 4 steps each at least).
+  w.dx_pairs = M > 128 && K > 128;
+  const int64_t tiles = w.dx_pairs ? tg_tiles(M, K, 1, false, 256, 256)
+                                   : tg_tiles(M, K, 1, false, 128, 128);
+  const int64_t slots = w.dx_pairs ? kPlanSms / 2 : kPlanSms;
+  const int64_t steps = ceil_div(std::min(w.cols, V), kTgKStep);
+  w.dx_split = 1;
+  double best = static_cast<double>(ceil_div(tiles, slots));
+  for (int s = 2; s <= 16 && steps / s >= 4 && tiles < 2 * slots; ++s) {
+    const double cost = static_cast<double>(ceil_div(tiles * s, slots)) / s;
+    if (cost < 0.9 * best) {
+      best = cost;
+      w.dx_split = s;
+    }
+  }
+  // every slice has work: steps are dealt in equal parts, the last one short
+  const int64_t per = ceil_div(steps, w.dx_split);
+  w.dx_split = static_cast<int>(ceil_div(steps, per));
+  size_t o = 0;
+  w.g = o;
+  o = align256(o + static_cast<size_t>(2 * M * w.cols));
+  w.acc = o;
+  if (w.pieces > 1) o = align256(o + static_cast<size_t>(4 * M * K));
+  w.part = o;
+  if (w.dx_split > 1) o = align256(o + static_cast<size_t>(4 * M * K * w.dx_split));
+  w.scale = o;
+  o = align256(o + 4);
+  w.total = o;
+  return w;
+}
+
+// -------------------------------------------------------- orthogonalisation
+
+constexpr int kOrthoMaxSteps = 32;
+// Largest smaller side that runs on both halves of its operands.
+constexpr int64_t kOrthoSplitN = 256;
+
+bitnet_status check_ortho_shape(int64_t B, int64_t N, int64_t K) {
+  if (B < 0 || N < 0 || K < 0) return BITNET_ERR_INVALID_ARG;
+  const int64_t n = std::min(N, K), k = std::max(N, K);
+  if (N < 1 || K < 1 || k > BITNET_MAX_K || B > 65535 ||
+      ceil_div(n, 128) * ceil_div(k, 128) > (1LL << 30) / std::max<int64_t>(B, 1))
+    return BITNET_ERR_UNSUPPORTED_SHAPE;
+  return BITNET_OK;
+}
+
+struct OrthoLayout {
+  int64_t n, k, ldx, ldr;
+  bool split;
+  int parts;                 // blocks of the norm, per matrix
+  size_t norm, X[2], X_lo[2], R, R_lo, Q, Q_lo, D, E, total;
+};
+
+OrthoLayout ortho_layout(int64_t B, int64_t N, int64_t K) {
+  OrthoLayout w{};
+  w.n = std::min(N, K);
+  w.k = std::max(N, K);
+  w.ldx = round_up(w.k, 64);
+  w.ldr = round_up(w.n, 64);
+  w.split = w.n <= kOrthoSplitN;
+  w.parts = static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>(ceil_div(N * K, 8 * kOrthoNormThreads), 4 * kPlanSms)));
+  size_t o = 0;
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o = align256(o + bytes);
+    return at;
+  };
+  const size_t x = static_cast<size_t>(2 * B * w.n * w.ldx);
+  const size_t r = static_cast<size_t>(2 * B * w.n * w.ldr);
+  w.norm = take(static_cast<size_t>(8 * B * w.parts));
+  for (int i = 0; i < 2; ++i) {
+    w.X[i] = take(x);
+    w.X_lo[i] = take(x);
+  }
+  w.R = take(r);
+  w.Q = take(r);
+  w.R_lo = take(w.split ? r : 0);
+  w.Q_lo = take(w.split ? r : 0);
+  w.D = take(static_cast<size_t>(4 * B * w.n));
+  w.E = take(static_cast<size_t>(4 * B * w.n));
+  w.total = o;
+  return w;
+}
+
+// The largest |a s + b s^3 + c s^5| and |b t + c t^2| for s in [0, top],
+// t = s^2: bounds of the next X and of b A + c A A.
+void ortho_bounds(double a, double b, double c, double top, double* next, double* poly) {
+  auto value = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
+  double m = value(top);
+  // stationary points: a + 3 b t + 5 c t^2 = 0
+  auto at = [&](double t) {
+    if (t > 0.0 && t <= top * top) m = std::max(m, value(std::sqrt(t)));
+  };
+  if (c != 0.0) {
+    const double disc = 9.0 * b * b - 20.0 * a * c;
+    if (disc >= 0.0) {
+      at((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
+      at((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
+    }
+  } else if (b != 0.0) {
+    at(-a / (3.0 * b));
+  }
+  *next = m;
+  const double t = top * top;
+  double q = std::fabs(t * (b + c * t));
+  if (c != 0.0) {
+    const double v = -b / (2.0 * c);
+    if (v > 0.0 && v < t) q = std::max(q, std::fabs(v * (b + c * v)));
+  }
+  *poly = q;
+}
+
+// The power of two that brings values up to `top` below 2^15 (fp16 ends at
+// 65504; the slack covers the rounding that pushes a value past its bound).
+double fp16_scale(double top) {
+  if (!(top > 0.0)) top = 1.0;
+  const int e = 14 - static_cast<int>(std::ceil(std::log2(top)));
+  return std::ldexp(1.0, std::max(-40, std::min(40, e)));
+}
+
+}  // namespace
+}  // namespace bitnet
+
+extern "C" {
+
+BITNET_API size_t bitnet_cross_entropy_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+  if (check_ce_shape(M, V, K) != BITNET_OK || M == 0) return 0;
+  return ce_fwd_layout(M, V).total;
+}
+
+BITNET_API bitnet_status bitnet_cross_entropy_forward(const void* x, const void* W,
+                                                      const int64_t* targets, int64_t M,
+                                                      int64_t V, int64_t K, float* loss,
+                                                      float* lse, void* workspace,
+                                                      size_t workspace_bytes,
+                                                      bitnet_stream_t stream) {
+  bitnet_status st = check_ce_shape(M, V, K);
+  if (st != BITNET_OK) return st;
+  if (M == 0) return BITNET_OK;
+  if (!x || !W || !targets || !loss || !lse) return BITNET_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(loss, 4) ||
+      !aligned(lse, 4))
+    return BITNET_ERR_MISALIGNED;
+  const CeFwdLayout L = ce_fwd_layout(M, V);
+  if (!workspace || workspace_bytes < L.total) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_MISALIGNED;
+  DeviceState* ds = device_state();
+  if (!ds) return BITNET_ERR_CUDA;
+  cudaStream_t s = as_stream(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  TgProblem g;
+  g.a.p = x;
+  g.a.ld = K;
+  g.b.p = W;
+  g.b.ld = K;
+  g.M = M;
+  g.N = V;
+  g.Kc = K;
+  CeStats::Params ep{targets, reinterpret_cast<float2*>(ws + L.part),
+                     reinterpret_cast<float*>(ws + L.logit)};
+  st = launch_tg<CeStats>(*ds, g, L.pairs, ep, s);
+  if (st != BITNET_OK) return st;
+  return launch_pdl(ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(M, 32))), 1024, s, ep.part,
+                    static_cast<int>(L.parts), ep.target_logit, targets, V, static_cast<int>(M),
+                    loss, lse);
+}
+
+BITNET_API size_t bitnet_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+  if (check_ce_shape(M, V, K) != BITNET_OK || M == 0) return 0;
+  return ce_bwd_layout(M, V, K).total;
+}
+
+BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void* W,
+                                                       const int64_t* targets, const float* lse,
+                                                       const float* dloss, int64_t M, int64_t V,
+                                                       int64_t K, void* dx, void* dW,
+                                                       void* workspace, size_t workspace_bytes,
+                                                       bitnet_stream_t stream) {
+  bitnet_status st = check_ce_shape(M, V, K);
+  if (st != BITNET_OK) return st;
+  if (dW && !aligned(dW, 16)) return BITNET_ERR_MISALIGNED;
+  cudaStream_t s = as_stream(stream);
+  if (M == 0) {
+    if (dW) return cuda_status(cudaMemsetAsync(dW, 0, 2 * static_cast<size_t>(V * K), s));
+    return BITNET_OK;
+  }
+  if (!x || !W || !targets || !lse || !dloss) return BITNET_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(lse, 4) ||
+      !aligned(dloss, 4) || (dx && !aligned(dx, 16)))
+    return BITNET_ERR_MISALIGNED;
+  const CeBwdLayout L = ce_bwd_layout(M, V, K);
+  if (!workspace || workspace_bytes < L.total) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_MISALIGNED;
+  if (!dx && !dW) return BITNET_OK;
+  DeviceState* ds = device_state();
+  if (!ds) return BITNET_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  __nv_bfloat16* gbuf = reinterpret_cast<__nv_bfloat16*>(ws + L.g);
+  float* acc = reinterpret_cast<float*>(ws + L.acc);
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  float* scale = reinterpret_cast<float*>(ws + L.scale);
+  st = launch_pdl(ce_scale_kernel, dim3(1), 1024, s, dloss, targets, V, M, scale);
+  if (st != BITNET_OK) return st;
+  for (int64_t i = 0; i < L.pieces; ++i) {
+    const int64_t v0 = i * L.cols, cols = std::min(L.cols, V - v0);
+    const __nv_bfloat16* Wi = static_cast<const __nv_bfloat16*>(W) + v0 * K;
+    {  // g of the piece
+      TgProblem g;
+      g.a.p = x;
+      g.a.ld = K;
+      g.b.p = Wi;
+      g.b.ld = K;
+      g.M = M;
+      g.N = cols;
+      g.Kc = K;
+      CeGrad::Params ep{targets, lse, dloss, scale, V, v0, gbuf, L.cols};
+      st = launch_tg<CeGrad>(*ds, g, tg_use_pairs(M, cols, 1, false), ep, s);
+      if (st != BITNET_OK) return st;
+    }
+    if (dx) {  // dx (+)= g W_i
+      const bool first = i == 0, last = i == L.pieces - 1;
+      TgProblem g;
+      g.a.p = gbuf;
+      g.a.ld = L.cols;
+      g.b.p = Wi;
+      g.b.ld = K;
+      g.b.mn = true;
+      g.M = M;
+      g.N = K;
+      g.Kc = cols;
+      const int64_t steps = ceil_div(cols, kTgKStep);
+      const int64_t per = ceil_div(steps, L.dx_split);
+      g.ksplit = static_cast<int>(ceil_div(steps, per));
+      TgStore::Params ep{};
+      ep.scale = scale;
+      ep.ld = K;
+      if (g.ksplit > 1) {
+        ep.f32 = part;
+        ep.split_stride = M * K;
+      } else {
+        ep.add = first ? nullptr : acc;
+        ep.f32 = acc;
+        ep.bf16 = last ? static_cast<__nv_bfloat16*>(dx) : nullptr;
+        ep.ld_out = K;
+      }
+      st = launch_tg<TgStore>(*ds, g, L.dx_pairs, ep, s);
+      if (st != BITNET_OK) return st;
+      if (g.ksplit > 1) {
+        const int64_t n4 = M * K / 4;
+        const int64_t blocks = std::min<int64_t>(ceil_div(n4, 256), 8LL * ds->num_sms);
+        st = launch_pdl(ce_join_dx_kernel, dim3(static_cast<unsigned>(blocks)), 256, s, part,
+                        g.ksplit, M * K, first ? nullptr : acc, n4, acc, scale,
+                        last ? static_cast<__nv_bfloat16*>(dx) : nullptr);
+        if (st != BITNET_OK) return st;
+      }
+    }
+    if (dW) {  // dW_i = g^T x
+      TgProblem g;
+      g.a.p = gbuf;
+      g.a.ld = L.cols;
+      g.a.mn = true;
+      g.b.p = x;
+      g.b.ld = K;
+      g.b.mn = true;
+      g.M = cols;
+      g.N = K;
+      g.Kc = M;
+      TgStore::Params ep{};
+      ep.scale = scale;
+      ep.bf16 = static_cast<__nv_bfloat16*>(dW) + v0 * K;
+      ep.ld_out = K;
+      st = launch_tg<TgStore>(*ds, g, tg_use_pairs(cols, K, 1, false), ep, s);
+      if (st != BITNET_OK) return st;
+    }
+  }
+  return BITNET_OK;
+}
+
+BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K) {
+  if (check_ortho_shape(B, N, K) != BITNET_OK || B == 0) return 0;
+  return ortho_layout(B, N, K).total;
+}
+
+BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_t B, int64_t N,
+                                              int64_t K, int steps, const double* coefficients,
+                                              float eps, void* O, void* workspace,
+                                              size_t workspace_bytes, bitnet_stream_t stream) {
+  bitnet_status st = check_ortho_shape(B, N, K);
+  if (st != BITNET_OK) return st;
+  if (steps < 1 || steps > kOrthoMaxSteps || !coefficients || !ok_dtype(u_dtype) ||
+      !(eps >= 0.0f) || eps > 3.0e38f)
+    return BITNET_ERR_INVALID_ARG;
+  // The scales of every step, from what its singular values can reach.
+  double top[kOrthoMaxSteps + 1], poly[kOrthoMaxSteps];
+  top[0] = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    const double* c = coefficients + 3 * i;
+    if (!std::isfinite(c[0]) || !std::isfinite(c[1]) || !std::isfinite(c[2]))
+      return BITNET_ERR_INVALID_ARG;
+    ortho_bounds(c[0], c[1], c[2], top[i], &top[i + 1], &poly[i]);
+    if (!(top[i + 1] <= 1048576.0) || !(poly[i] <= 1048576.0)) return BITNET_ERR_INVALID_ARG;
+  }
+  if (B == 0) return BITNET_OK;
+  if (!U || !O) return BITNET_ERR_INVALID_ARG;
+  if (!aligned(U, 16) || !aligned(O, 16)) return BITNET_ERR_MISALIGNED;
+  const OrthoLayout L = ortho_layout(B, N, K);
+  if (!workspace || workspace_bytes < L.total) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_MISALIGNED;
+  DeviceState* ds = device_state();
+  if (!ds) return BITNET_ERR_CUDA;
+  cudaStream_t s = as_stream(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto half_at = [ws](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
+  const bool tall = N > K;
+  const int u_bf16 = u_dtype == BITNET_BF16 ? 1 : 0;
+  double* norm = reinterpret_cast<double*>(ws + L.norm);
+  float* D = reinterpret_cast<float*>(ws + L.D);
+  float* E = reinterpret_cast<float*>(ws + L.E);
+  uint16_t* R_lo = L.split ? half_at(L.R_lo) : nullptr;
+  uint16_t* Q_lo = L.split ? half_at(L.Q_lo) : nullptr;
+  const int64_t xb = L.n * L.ldx, rb = L.n * L.ldr;
+
+  st = launch_pdl(ortho_norm_kernel,
+                  dim3(static_cast<unsigned>(L.parts), static_cast<unsigned>(B)),
+                  kOrthoNormThreads, s, U, u_bf16, N * K, norm);
+  if (st != BITNET_OK) return st;
+  double sx = fp16_scale(top[0]);
+  st = launch_pdl(ortho_start_kernel,
+                  dim3(static_cast<unsigned>(ceil_div(K, 32)),
+                       static_cast<unsigned>(ceil_div(N, 32)), static_cast<unsigned>(B)),
+                  256, s, U, u_bf16, static_cast<int>(N), static_cast<int>(K), tall ? 1 : 0, norm,
+                  L.parts, eps, static_cast<float>(sx), half_at(L.X[0]), half_at(L.X_lo[0]),
+                  L.ldx, xb);
+  if (st != BITNET_OK) return st;
+
+  const bool sym_pairs = tg_use_pairs(L.n, L.n, B, true);
+  const bool x_pairs = tg_use_pairs(L.n, L.k, B, false);
+  for (int i = 0; i < steps; ++i) {
+    const double* c = coefficients + 3 * i;
+    const int from = i & 1, to = from ^ 1;
+    const double sr = fp16_scale(top[i] * top[i]), sq = fp16_scale(poly[i]);
+    const double sy = fp16_scale(top[i + 1]);
+    TgProblem g;
+    g.bf16 = false;
+    g.batch = B;
+    g.passes = L.split ? 3 : 1;
+    // A = X X^T
+    g.M = g.N = L.n;
+    g.Kc = L.k;
+    g.sym = true;
+    g.a.p = half_at(L.X[from]);
+    g.a.lo = half_at(L.X_lo[from]);
+    g.a.ld = L.ldx;
+    g.a.batch_stride = xb;
+    g.b = g.a;
+    OrthoGram::Params gram{D, half_at(L.R), R_lo, L.ldr, rb, static_cast<float>(1.0 / (sx * sx)),
+                           static_cast<float>(sr / (sx * sx))};
+    st = launch_tg<OrthoGram>(*ds, g, sym_pairs, gram, s);
+    if (st != BITNET_OK) return st;
+    // R R -> Q, E
+    g.Kc = L.n;
+    g.a.p = half_at(L.R);
+    g.a.lo = R_lo;
+    g.a.ld = L.ldr;
+    g.a.batch_stride = rb;
+    g.b = g.a;
+    OrthoPoly::Params poly_p{D, E, half_at(L.R), R_lo, half_at(L.Q), Q_lo, L.ldr, rb,
+                             static_cast<float>(c[0]), static_cast<float>(c[1]),
+                             static_cast<float>(c[2]), static_cast<float>(1.0 / (sr * sr)),
+                             static_cast<float>(1.0 / sr), static_cast<float>(sq)};
+    st = launch_tg<OrthoPoly>(*ds, g, sym_pairs, poly_p, s);
+    if (st != BITNET_OK) return st;
+    // X <- E X + Q X
+    g.sym = false;
+    g.N = L.k;
+    g.a.p = half_at(L.Q);
+    g.a.lo = Q_lo;
+    g.b.p = half_at(L.X[from]);
+    g.b.lo = half_at(L.X_lo[from]);
+    g.b.ld = L.ldx;
+    g.b.batch_stride = xb;
+    g.b.mn = true;
+    const bool last = i == steps - 1;
+    OrthoUpdate::Params up{E, half_at(L.X[from]), half_at(L.X_lo[from]),
+                           last ? nullptr : half_at(L.X[to]), half_at(L.X_lo[to]), L.ldx, xb,
+                           static_cast<__nv_bfloat16*>(O), tall ? 1 : 0,
+                           static_cast<float>(1.0 / (sq * sx)), static_cast<float>(1.0 / sx),
+                           static_cast<float>(sy)};
+    st = launch_tg<OrthoUpdate>(*ds, g, x_pairs, up, s);
+    if (st != BITNET_OK) return st;
+    sx = sy;
+  }
+  return BITNET_OK;
+}
+
+}  // extern "C"
