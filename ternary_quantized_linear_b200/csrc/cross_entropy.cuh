@@ -7,9 +7,14 @@
 //   g_mv   = dloss_m (exp(z_mv - lse_m) - [v = t(m)]), 0 where t(m) is not in [0, V)
 //   dx = g W,  dW = g^T x
 //
-// Forward: one product whose epilogue keeps, per row and column half of a
-// tile, the running maximum and the sum of exp(z - maximum) (fp32), and the
-// target's logit; a second kernel joins them.  The logits never leave the SM.
+// Forward: one product whose epilogue keeps, per row and half of a tile's
+// columns, the running maximum and the sum of exp(z - maximum) (fp32) of all
+// but the target's logit; a second kernel joins them.  The logits never leave
+// the SM.  The target's logit is a dot product of its own, in fp32 with
+// rounded sums (the tensor cores truncate theirs, which at 4096 terms moves a
+// logit by some 1e-6 of itself): with s the sum of exp(z_v - z_t) over the
+// others, loss = log(1 + s) has no cancellation for a confident token, and
+// the target's entry of the gradient is exp(z_t - lse) - 1 by expm1.
 // Backward: the vocabulary is taken in pieces; the same product forms g of a
 // piece (bf16, in the workspace) from the saved lse, and two more give dx
 // (summed over the pieces in fp32) and the piece's rows of dW.
@@ -36,28 +41,57 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Logit of one row's target, by one warp: products of bf16 are exact in fp32,
+// each lane sums its own 8-element pieces in order.
+__device__ __forceinline__ float ce_target_dot(const __nv_bfloat16* __restrict__ x,
+                                               const __nv_bfloat16* __restrict__ w, int64_t K,
+                                               int lane) {
+  float s = 0.0f;
+  for (int64_t i = lane; i < (K >> 3); i += 32) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(w) + i);
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s = __fmaf_rn(bf16_bits_to_f32(av[j] & 0xFFFFu), bf16_bits_to_f32(bv[j] & 0xFFFFu), s);
+      s = __fmaf_rn(bf16_bits_to_f32(av[j] >> 16), bf16_bits_to_f32(bv[j] >> 16), s);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  return s;
+}
+
 struct CeStats {
+  static constexpr int kSlots = 0, kSlotBytes = 0;
   struct Params {
     const int64_t* targets;
     float2* part;          // [2 nt][M]: maximum, sum of exp(z - maximum)
-    float* target_logit;   // [M], written for valid targets only
   };
-  template <int COLS>
-  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgPart& t) {
-    const bool live = t.row < p.M;
-    const int64_t target = live ? __ldg(e.targets + t.row) : -1;
+  static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
+                                               const TgPart&) {}
+  static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps&,
+                                             const TgPart& t, TgStage&, Src src) {
+    const int64_t target = t.live ? __ldg(e.targets + t.row) : -1;
     float mx = -INFINITY, sum = 0.0f;
+    const int n = t.chunks();
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      const int col = t.col0 + c;
-      if (col >= p.N) break;  // the same for all of the warp
+    for (int k = 0; k < n; ++k) {
+      const int c = t.first + k * t.step, col = t.col0 + c;
       uint32_t r[32];
-      tmem_ld_32x32b_x32(t.tmem + c, r);
-      tmem_ld_wait();
-      if (col + 32 > p.N) {
+      src.load(c, r);
+      if (col + 32 > t.col_end) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (col + i >= p.N) r[i] = 0xFF800000u;  // -inf: past the vocabulary
+          if (col + i >= t.col_end) r[i] = 0xFF800000u;  // -inf: not this tile's
+      }
+      if (target >= col && target < t.col_end && target < col + 32) {
+        const int at = static_cast<int>(target) - col;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i == at) r[i] = 0xFF800000u;
       }
       float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -68,37 +102,43 @@ struct CeStats {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         s4[i & 3] += exp2_approx(__fmaf_rn(__uint_as_float(r[i]), kLog2e, -shift));
-      // A row of -inf so far: nothing to sum, and no inf - inf.
       if (m_new != -INFINITY) {
         sum = __fmaf_rn(sum, exp2_approx(__fmaf_rn(mx, kLog2e, -shift)),
                         (s4[0] + s4[1]) + (s4[2] + s4[3]));
         mx = m_new;
-      }
-      if (target >= col && target < col + 32 && target < p.N) {
-        const int at = static_cast<int>(target) - col;
-        float z = 0.0f;
+      } else {  // -inf and NaN only: no inf - inf, but NaN stays
+        float nan = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (i == at) z = __uint_as_float(r[i]);
-        e.target_logit[t.row] = z;
+          if (__uint_as_float(r[i]) != -INFINITY) nan = __uint_as_float(r[i]);
+        sum += nan;
       }
     }
-    if (live)
-      e.part[(2 * static_cast<int64_t>(t.tile.n) + t.half) * p.M + t.row] = make_float2(mx, sum);
+    if (t.live)
+      e.part[(2 * static_cast<int64_t>(t.tile.n) + (t.first >> 5)) * p.M + t.row] =
+          make_float2(mx, sum);
   }
 };
 
 // Joins the parts of each row: 32 rows x 32 lanes of parts per block (parts
-// of neighbouring rows are neighbours in memory).
+// of neighbouring rows are neighbours in memory); warp w also forms the
+// target's logit of row w.
 __global__ void __launch_bounds__(1024)
-ce_join_kernel(const float2* __restrict__ part, int parts, const float* __restrict__ target_logit,
-               const int64_t* __restrict__ targets, int64_t V, int M, float* __restrict__ loss,
-               float* __restrict__ lse) {
-  __shared__ float smx[32][33], ssum[32][33];
+ce_join_kernel(const float2* __restrict__ part, int parts, const __nv_bfloat16* __restrict__ x,
+               const __nv_bfloat16* __restrict__ W, const int64_t* __restrict__ targets,
+               int64_t V, int64_t K, int M, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float smx[32][33], ssum[32][33], slogit[32];
   const int r = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 32 + r;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
+  {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + w;
+    const int64_t t = row < M ? targets[row] : -1;
+    float z = 0.0f;
+    if (t >= 0 && t < V) z = ce_target_dot(x + row * K, W + t * K, K, r);
+    if (r == 0) slogit[w] = z;
+  }
   float mx = -INFINITY, sum = 0.0f;
   auto join = [&](float pm, float ps) {
     const float m_new = fmaxf(mx, pm);
@@ -106,9 +146,12 @@ ce_join_kernel(const float2* __restrict__ part, int parts, const float* __restri
       sum = __fmaf_rn(sum, exp2_approx((mx - m_new) * kLog2e),
                       ps * exp2_approx((pm - m_new) * kLog2e));
       mx = m_new;
+    } else {
+      sum += ps;  // 0, or NaN
     }
   };
   if (m < M)
+#pragma unroll 4
     for (int i = w; i < parts; i += 32) {
       const float2 v = part[static_cast<int64_t>(i) * M + m];
       join(v.x, v.y);
@@ -118,82 +161,112 @@ ce_join_kernel(const float2* __restrict__ part, int parts, const float* __restri
   __syncthreads();
   if (w == 0 && m < M) {
     for (int i = 1; i < 32; ++i) join(smx[i][r], ssum[i][r]);
-    const float l = mx + logf(sum);
-    lse[m] = l;
     const int64_t t = targets[m];
-    loss[m] = (t >= 0 && t < V) ? l - target_logit[m] : 0.0f;
+    if (t >= 0 && t < V) {
+      // mx, sum leave out the target: loss = log(1 + sum exp(mx - z))
+      const float z = slogit[r], d = mx - z;
+      float l;
+      if (mx == -INFINITY && sum == 0.0f)
+        l = z - z;  // no other entry with any weight (NaN for a non-finite z)
+      else
+        l = d <= 0.0f ? log1pf(sum * expf(d)) : d + logf(sum + expf(-d));
+      loss[m] = l;
+      lse[m] = z + l;
+    } else {
+      loss[m] = 0.0f;
+      lse[m] = mx + logf(sum);
+    }
   }
 }
 
-// scale = max |dloss| over the tokens that have a target; one block.
-__global__ void __launch_bounds__(1024)
-ce_scale_kernel(const float* __restrict__ dloss, const int64_t* __restrict__ targets, int64_t V,
-                int64_t M, float* __restrict__ scale) {
-  __shared__ float red[32];
+// Per row: the target's logit.  Block 0 also: max |dloss| over the rows that
+// have a target.
+__global__ void __launch_bounds__(256)
+ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ W,
+                 const int64_t* __restrict__ targets, const float* __restrict__ dloss, int64_t M,
+                 int64_t V, int64_t K, float* __restrict__ logit, float* __restrict__ scale) {
+  __shared__ float red[8];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + w;
+  if (row < M) {
+    const int64_t t = targets[row];
+    if (t >= 0 && t < V) {
+      const float z = ce_target_dot(x + row * K, W + t * K, K, lane);
+      if (lane == 0) logit[row] = z;
+    }
+  }
+  if (blockIdx.x != 0) return;
   float a = 0.0f;
-  for (int64_t m = threadIdx.x; m < M; m += 1024) {
+  for (int64_t m = threadIdx.x; m < M; m += 256) {
     const int64_t t = targets[m];
     if (t >= 0 && t < V) a = fmaxf(a, fabsf(dloss[m]));  // NaN: its own row carries it
   }
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  if (lane == 0) red[w] = a;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    a = red[threadIdx.x];
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    if (threadIdx.x == 0) *scale = a;
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) a = fmaxf(a, red[i]);
+    *scale = a;
   }
 }
 
 struct CeGrad {
+  static constexpr int kSlots = 2, kSlotBytes = 2048;
   struct Params {
     const int64_t* targets;
     const float* lse;
     const float* dloss;
+    const float* logit;    // of the target
     const float* scale;    // max |dloss|: g is formed relative to it
     int64_t V;             // of the whole vocabulary
     int64_t v0;            // first column of this piece
-    __nv_bfloat16* g;      // [M][ld], ld a multiple of 32 and >= the piece
-    int64_t ld;
   };
-  template <int COLS>
-  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgPart& t) {
-    const bool live = t.row < p.M;
-    int64_t target = live ? __ldg(e.targets + t.row) : -1;
+  static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
+                                               const TgPart&) {}
+  static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape&, const TgMaps& m,
+                                             const TgPart& t, TgStage& st, Src src) {
+    int64_t target = t.live ? __ldg(e.targets + t.row) : -1;
     const bool valid = target >= 0 && target < e.V;
-    const float top = __ldg(e.scale);
-    const float dl = valid ? __ldg(e.dloss + t.row) : 0.0f;
-    const float d = dl == 0.0f ? 0.0f : __fdiv_rn(dl, top);
-    const float shift = valid ? __ldg(e.lse + t.row) * kLog2e : 0.0f;
-    target = valid ? target - e.v0 : -1;
+    float d = 0.0f, shift = 0.0f, at_target = 0.0f;
+    if (valid) {
+      const float dl = __ldg(e.dloss + t.row), l = __ldg(e.lse + t.row);
+      d = dl == 0.0f ? 0.0f : __fdiv_rn(dl, __ldcg(e.scale));
+      shift = l * kLog2e;
+      at_target = expm1f(__ldcg(e.logit + t.row) - l);
+      target -= e.v0;
+    }
+    const int n = t.chunks();
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      const int col = t.col0 + c;
-      if (col >= p.N) break;  // the same for all of the warp
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(t.tmem + c, r);
-      tmem_ld_wait();
-      const bool here = target >= col && target < col + 32;
-      uint32_t w[16];
+    for (int k = 0; k < n; ++k) {
+      const int c = t.first + k * t.step, col = t.col0 + c;
+      uint32_t r[32], w[16];
+      src.load(c, r);
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         r[i] = __float_as_uint(
             exp2_approx(__fmaf_rn(__uint_as_float(r[i]), kLog2e, -shift)));
-      if (here) {
+      if (valid && target >= col && target < col + 32) {
         const int at = static_cast<int>(target) - col;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (i == at) r[i] = __float_as_uint(__fadd_rn(__uint_as_float(r[i]), -1.0f));
+          if (i == at) r[i] = __float_as_uint(at_target);
       }
       // A row without a target has no gradient, whatever its logits hold.
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         w[i] = valid ? pack_bf16x2(__uint_as_float(r[2 * i]) * d, __uint_as_float(r[2 * i + 1]) * d)
                      : 0u;
-      if (live)
-        store_row32_16(reinterpret_cast<uint16_t*>(e.g) + t.row * e.ld + col, w, true, 32);
+      uint8_t* blk = tg_out_block<CeGrad>(st);
+      block16_write(blk, st.lane, w);
+      fence_proxy_async_smem();
+      __syncwarp();
+      tg_store_block(st, &m.out, blk, col, t);
+      if (st.lane == 0) bulk_commit();
     }
   }
 };

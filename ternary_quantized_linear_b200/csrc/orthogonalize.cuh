@@ -117,139 +117,173 @@ ortho_start_kernel(const void* __restrict__ U, int u_bf16, int rows, int cols, i
   }
 }
 
-// A symmetric product's tile: its rows, and for a tile below the diagonal the
-// mirrored ones (lanes hold neighbouring rows, so a mirrored store of one
-// column is 64 contiguous bytes).
-__device__ __forceinline__ void ortho_store_sym(uint16_t* base, int64_t ld, int row, int col,
-                                                const uint32_t (&w)[16], int n, int M,
-                                                bool mirror) {
-  if (row < M) {
-    // ld is a multiple of 32: the chunk's last columns may be padding.
-    store_row32_16(base + row * ld + col, w, true, 32);
-    if (mirror) {
+// Of a tile below the diagonal of a symmetric product, the mirrored entries:
+// lanes hold neighbouring rows, so a store of one column is 64 contiguous
+// bytes.
+__device__ __forceinline__ void ortho_store_mirror(uint16_t* base, int64_t ld, int row, int col,
+                                                   const uint32_t (&w)[16], int n) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n)
-          base[static_cast<int64_t>(col + i) * ld + row] =
-              static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-    }
+  for (int i = 0; i < 32; ++i)
+    if (i < n)
+      base[static_cast<int64_t>(col + i) * ld + row] =
+          static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ void ortho_pack(const float (&v)[32], uint32_t (&hi)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    hi[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
-__device__ __forceinline__ void ortho_pack(const float (&v)[32], uint32_t (&hi)[16],
-                                           uint32_t (&lo)[16]) {
+__device__ __forceinline__ float2 half2_bits_to_f32(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// What v has beyond hi.
+__device__ __forceinline__ void ortho_pack_rest(const float (&v)[32], const uint32_t (&hi)[16],
+                                                uint32_t (&lo)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    uint16_t h0, l0, h1, l1;
-    split_half(v[2 * i], h0, l0);
-    split_half(v[2 * i + 1], h1, l1);
-    hi[i] = h0 | (static_cast<uint32_t>(h1) << 16);
-    lo[i] = l0 | (static_cast<uint32_t>(l1) << 16);
+    const float2 f = half2_bits_to_f32(hi[i]);
+    const __half2 h = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    lo[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// A block (and the low halves behind it) out by TMA, mirrored when asked.
+__device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const TgPart& t,
+                                            uint8_t* blk, int col, const float (&v)[32],
+                                            bool low, bool mirror, uint16_t* base,
+                                            uint16_t* base_lo, int64_t ld, int N) {
+  uint32_t w[16], lo[16];
+  ortho_pack(v, w);
+  block16_write(blk, st.lane, w);
+  if (low) {
+    ortho_pack_rest(v, w, lo);
+    block16_write(blk + 2048, st.lane, lo);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  tg_store_block(st, &m.out, blk, col, t);
+  if (low) tg_store_block(st, &m.out_lo, blk + 2048, col, t);
+  if (st.lane == 0) bulk_commit();
+  if (mirror && t.live) {
+    ortho_store_mirror(base, ld, t.row, col, w, min(32, N - col));
+    if (low) ortho_store_mirror(base_lo, ld, t.row, col, lo, min(32, N - col));
   }
 }
 
 // A = X X^T: its diagonal to D (fp32), the rest to R (fp16, and its low half
 // where the products take it).
 struct OrthoGram {
+  static constexpr int kSlots = 2, kSlotBytes = 4096;
   struct Params {
     float* D;              // [batch][n]
     uint16_t *R, *R_lo;    // [batch][n][ld]; R_lo may be null
     int64_t ld, batch;     // row stride, batch stride (elements)
     float to_true, to_R;   // accumulator -> A, accumulator -> stored R
   };
-  template <int COLS>
-  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgPart& t) {
+  static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
+                                               const TgPart&) {}
+  static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
+                                             const TgPart& t, TgStage& st, Src src) {
     const bool mirror = t.tile.m != t.tile.n;
+    const int64_t base = t.tile.b * e.batch;
+    const int n = t.chunks();
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      const int col = t.col0 + c;
-      if (col >= p.N) break;  // the same for all of the warp
+    for (int k = 0; k < n; ++k) {
+      const int c = t.first + k * t.step, col = t.col0 + c;
       uint32_t r[32];
-      tmem_ld_32x32b_x32(t.tmem + c, r);
-      tmem_ld_wait();
-      float v[32];
+      src.load(c, r);
+      float v[32], d = 0.0f;
+      const int at = t.row - col;  // the diagonal's place in the chunk
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float z = __uint_as_float(r[i]);
-        const bool diag = col + i == t.row;
-        if (diag && t.row < p.M)
-          e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = z * e.to_true;
-        v[i] = diag ? 0.0f : z * e.to_R;
+        if (i == at) d = z;
+        v[i] = i == at ? 0.0f : z * e.to_R;
       }
-      uint32_t hi[16], lo[16];
-      ortho_pack(v, hi, lo);
-      const int n = min(32, p.N - col);
-      ortho_store_sym(e.R + t.tile.b * e.batch, e.ld, t.row, col, hi, n, p.M, mirror);
-      if (e.R_lo)
-        ortho_store_sym(e.R_lo + t.tile.b * e.batch, e.ld, t.row, col, lo, n, p.M, mirror);
+      if (t.live && at >= 0 && at < 32)
+        e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.to_true;
+      ortho_store(st, m, t, tg_out_block<OrthoGram>(st), col, v, e.R_lo != nullptr, mirror,
+                  e.R + base, e.R_lo + base, e.ld, p.N);
     }
   }
 };
 
 // R R, and from it Q (fp16) and a + E (fp32, the factor of X).
 struct OrthoPoly {
+  static constexpr int kSlots = 3, kSlotBytes = 4096;
   struct Params {
     const float* D;
     float* E;              // [batch][n]: a + b D + c (D^2 + (R R)_ii)
-    const uint16_t *R, *R_lo;
-    uint16_t *Q, *Q_lo;    // Q_lo may be null
+    uint16_t *Q, *Q_lo;    // Q_lo may be null (then R has no low half either)
     int64_t ld, batch;
     float a, b, c;
     float acc_true, r_true, to_Q;
   };
-  template <int COLS>
-  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgPart& t) {
-    const bool mirror = t.tile.m != t.tile.n;
-    const bool live = t.row < p.M;
+  using In = TgInput<OrthoPoly>;
+  static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
+                                               const TgPart& t) {
+    In::begin(st, m, t, e.Q_lo != nullptr, 2048);
+  }
+  static __device__ __forceinline__ void abandon(TgStage& st, const Params&, const TgPart& t) {
+    In::abandon(st, t);
+  }
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
+                                             const TgPart& t, TgStage& st, Src src) {
+    const bool mirror = t.tile.m != t.tile.n, low = e.Q_lo != nullptr;
     const float* D = e.D + static_cast<int64_t>(t.tile.b) * p.M;
-    const float di = live ? D[t.row] : 0.0f;
+    const float di = t.live ? __ldcg(D + t.row) : 0.0f;
     const int64_t base = t.tile.b * e.batch;
+    const int n = t.chunks();
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      const int col = t.col0 + c;
-      if (col >= p.N) break;  // the same for all of the warp
-      uint32_t rh[16], rl[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) rh[i] = rl[i] = 0u;
-      if (live) {
-        const uint4* s = reinterpret_cast<const uint4*>(e.R + base + t.row * e.ld + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = s[i];
-          rh[4 * i] = w.x; rh[4 * i + 1] = w.y; rh[4 * i + 2] = w.z; rh[4 * i + 3] = w.w;
-        }
-        if (e.R_lo) {
-          const uint4* sl = reinterpret_cast<const uint4*>(e.R_lo + base + t.row * e.ld + col);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 w = sl[i];
-            rl[4 * i] = w.x; rl[4 * i + 1] = w.y; rl[4 * i + 2] = w.z; rl[4 * i + 3] = w.w;
-          }
-        }
-      }
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(t.tmem + c, r);
-      tmem_ld_wait();
+    for (int k = 0; k < n; ++k) {
+      const int c = t.first + k * t.step, col = t.col0 + c;
+      const float dl = !t.dry && col + st.lane < p.N ? __ldcg(D + col + st.lane) : 0.0f;
+      uint8_t* blk = st.base + (st.seq % kSlots) * kSlotBytes;
+      if (!In::wait(st, t, k)) break;
+      uint32_t r[32], w[16];
+      block16_read(blk, st.lane, w);
       float v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t sh = 16 * (i & 1);
-        const float rr = __uint_as_float(r[i]) * e.acc_true;
-        const float x = (half_bits_to_f32((rh[i >> 1] >> sh) & 0xFFFFu) +
-                         half_bits_to_f32((rl[i >> 1] >> sh) & 0xFFFFu)) * e.r_true;
-        const float dj = col + i < p.N ? __ldg(D + col + i) : 0.0f;
-        const bool diag = col + i == t.row;
-        const float q = __fmaf_rn(e.c, __fmaf_rn(di + dj, x, rr), e.b * x);
-        if (diag && live)
-          e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
-              e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr), e.b * di);
-        v[i] = diag ? 0.0f : q * e.to_Q;
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = half2_bits_to_f32(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
       }
-      uint32_t hi[16], lo[16];
-      ortho_pack(v, hi, lo);
-      const int n = min(32, p.N - col);
-      ortho_store_sym(e.Q + base, e.ld, t.row, col, hi, n, p.M, mirror);
-      if (e.Q_lo) ortho_store_sym(e.Q_lo + base, e.ld, t.row, col, lo, n, p.M, mirror);
+      if (low) {
+        block16_read(blk + 2048, st.lane, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = half2_bits_to_f32(w[i]);
+          v[2 * i] += f.x;
+          v[2 * i + 1] += f.y;
+        }
+      }
+      src.load(c, r);
+      const int at = t.row - col;  // the diagonal's place in the chunk
+      float rr_ii = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float rr = __uint_as_float(r[i]) * e.acc_true;
+        const float x = v[i] * e.r_true;
+        const float dj = __shfl_sync(0xFFFFFFFFu, dl, i);
+        if (i == at) rr_ii = rr;
+        v[i] = i == at ? 0.0f
+                       : __fmaf_rn(e.c, __fmaf_rn(di + dj, x, rr), e.b * x) * e.to_Q;
+      }
+      if (t.live && at >= 0 && at < 32)
+        e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
+            e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr_ii), e.b * di);
+      __syncwarp();  // the whole block was read
+      ortho_store(st, m, t, blk, col, v, low, mirror, e.Q + base, e.Q_lo + base, e.ld, p.N);
+      In::next(st, m, t, k, low, 2048);
     }
   }
 };
@@ -257,75 +291,83 @@ struct OrthoPoly {
 // X <- (a + E_i) X + Q X: the next X as two halves, or the result in bf16
 // (transposed back for a tall update).
 struct OrthoUpdate {
+  static constexpr int kSlots = 3, kSlotBytes = 4096;
   struct Params {
     const float* E;
-    const uint16_t *X, *X_lo;
-    uint16_t *Y, *Y_lo;    // next X, or null for the last step
-    int64_t ld, batch;     // of X and Y
-    __nv_bfloat16* out;    // last step: [batch][n][k], or [batch][k][n] when tall
+    __nv_bfloat16* out;    // last step: [batch][n][k], or [batch][k][n] when tall; else null
     int tall;
+    int direct;            // store the result without `maps.out` (rows of odd length)
     float acc_true, x_true, to_Y;
   };
-  template <int COLS>
-  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgPart& t) {
-    const bool live = t.row < p.M;
-    const float ei = live ? e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] : 0.0f;
-    const int64_t base = t.tile.b * e.batch;
+  using In = TgInput<OrthoUpdate>;
+  static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params&,
+                                               const TgPart& t) {
+    In::begin(st, m, t, true, 2048);
+  }
+  static __device__ __forceinline__ void abandon(TgStage& st, const Params&, const TgPart& t) {
+    In::abandon(st, t);
+  }
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
+                                             const TgPart& t, TgStage& st, Src src) {
+    const float ei =
+        t.live ? __ldcg(e.E + static_cast<int64_t>(t.tile.b) * p.M + t.row) * e.x_true : 0.0f;
+    const int n = t.chunks();
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      const int col = t.col0 + c;
-      if (col >= p.N) break;  // the same for all of the warp
-      uint32_t xh[16], xl[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) xh[i] = xl[i] = 0u;
-      if (live) {
-        const uint4* s = reinterpret_cast<const uint4*>(e.X + base + t.row * e.ld + col);
-        const uint4* sl = reinterpret_cast<const uint4*>(e.X_lo + base + t.row * e.ld + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = s[i], u = sl[i];
-          xh[4 * i] = w.x; xh[4 * i + 1] = w.y; xh[4 * i + 2] = w.z; xh[4 * i + 3] = w.w;
-          xl[4 * i] = u.x; xl[4 * i + 1] = u.y; xl[4 * i + 2] = u.z; xl[4 * i + 3] = u.w;
-        }
-      }
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(t.tmem + c, r);
-      tmem_ld_wait();
+    for (int k = 0; k < n; ++k) {
+      const int c = t.first + k * t.step, col = t.col0 + c;
+      uint8_t* blk = st.base + (st.seq % kSlots) * kSlotBytes;
+      if (!In::wait(st, t, k)) break;
+      uint32_t r[32], w[16];
       float v[32];
+      block16_read(blk, st.lane, w);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t sh = 16 * (i & 1);
-        const float x = (half_bits_to_f32((xh[i >> 1] >> sh) & 0xFFFFu) +
-                         half_bits_to_f32((xl[i >> 1] >> sh) & 0xFFFFu)) * e.x_true;
-        v[i] = __fmaf_rn(ei, x, __uint_as_float(r[i]) * e.acc_true);
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = half2_bits_to_f32(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
       }
-      const int n = min(32, p.N - col);
-      if (e.Y) {
-        uint32_t hi[16], lo[16];
+      block16_read(blk + 2048, st.lane, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = half2_bits_to_f32(w[i]);
+        v[2 * i] += f.x;
+        v[2 * i + 1] += f.y;
+      }
+      src.load(c, r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = __fmaf_rn(ei, v[i], __uint_as_float(r[i]) * e.acc_true);
+      __syncwarp();  // the whole block was read
+      if (!e.out) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= e.to_Y;
-        ortho_pack(v, hi, lo);
-        if (live) {
-          store_row32_16(e.Y + base + t.row * e.ld + col, hi, true, 32);
-          store_row32_16(e.Y_lo + base + t.row * e.ld + col, lo, true, 32);
-        }
+        ortho_store(st, m, t, blk, col, v, true, false, nullptr, nullptr, 0, p.N);
       } else {
-        uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
         uint16_t* out = reinterpret_cast<uint16_t*>(e.out) +
                         static_cast<int64_t>(t.tile.b) * p.M * p.N;
-        if (live && !e.tall) {
-          store_row32_16(out + static_cast<int64_t>(t.row) * p.N + col, w,
-                         n == 32 && (p.N & 7) == 0, n);
-        } else if (live) {
+        const int cols = min(32, p.N - col);
+        if (e.tall) {
+          if (t.live) ortho_store_mirror(out, p.M, t.row, col, w, cols);
+        } else if (e.direct) {
+          if (t.live) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < n)
-              out[static_cast<int64_t>(col + i) * p.M + t.row] =
-                  static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+            for (int i = 0; i < 32; ++i)
+              if (i < cols)
+                out[static_cast<int64_t>(t.row) * p.N + col + i] =
+                    static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+          }
+        } else {
+          block16_write(blk, st.lane, w);
+          fence_proxy_async_smem();
+          __syncwarp();
+          tg_store_block(st, &m.out, blk, col, t);
         }
+        if (st.lane == 0) bulk_commit();
       }
+      In::next(st, m, t, k, true, 2048);
     }
   }
 };

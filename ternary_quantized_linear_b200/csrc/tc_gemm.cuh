@@ -10,18 +10,34 @@
 // operators needs a transposed copy.  `passes` = 3 sums A B + A B_lo + A_lo B
 // for operands held as a high and a low half.
 //
-// Layout of the work: an output tile is (128 CG) x BN.  CG = 2 pairs two SMs
-// on one 256-row tile (cta_group::2): each CTA holds its own 128 rows of A
-// and half of B's rows, so a byte of B in shared memory feeds twice the MMA
-// work; CG = 1 is for outputs with few tiles.  Tiles are dealt round-robin to
-// a grid of resident CTAs; the accumulator is double-buffered in TMEM, so a
-// tile's epilogue runs under the next tile's MMAs.
+// Layout of the work: an output tile is (128 CG) x bn, bn <= BN.  CG = 2 pairs
+// two SMs on one 256-row tile (cta_group::2): each CTA holds its own 128 rows
+// of A and half of B's rows, so a byte of B in shared memory feeds twice the
+// MMA work; CG = 1 is for outputs with few tiles.  An SM takes 64 bytes a
+// cycle from L2, and a 64-k step of a 256 x 256 pair tile needs 32 KiB per SM
+// and 512 cycles of MMA: both just meet, while a 128 x 128 tile, with as many
+// bytes for half the MMA work, runs at half the rate.  SPLIT = 2 or 4
+// (CG = 1) lets a cluster of CTAs share one tile's contraction: each sums its
+// part, the parts meet through distributed shared memory, added in rank
+// order, and each CTA finishes its share of the columns.
+//
+// Tiles are dealt round-robin to a grid of resident CTAs; the accumulator is
+// double-buffered in TMEM, so a tile's epilogue runs under the next tile's
+// MMAs.
 //
 // Warps: 0 copies (TMA, one thread, a ring of 64-k stages), 1 issues the MMAs
-// (the pair's leader only), 2 owns TMEM, 4..11 run the epilogue: warp w reads
-// TMEM lanes 32 (w % 4) .. +31, and columns [0, BN/2) for w < 8, else the
-// other half.  Every wait is bounded; on a timeout the kernel records the
-// failure, lets its copies land and exits.
+// (the pair's leader only), 2 owns TMEM, 4..11 run the epilogue: warp w has
+// TMEM lanes 32 (w % 4) .. +31, and every other chunk of 32 columns.  The
+// epilogue's tensors pass through shared memory in 32 x 32 blocks, copied by
+// TMA: a warp's own loads and stores, one row per lane, cost 32 transactions
+// each and took longer than the MMAs of a short contraction.
+//
+// A kernel's first pass through its epilogue waits for its instructions to
+// arrive, about 5 us; the epilogue warps take that pass on an empty tile
+// (`dry`) while the first copies and MMAs are under way.
+//
+// Every wait is bounded; on a timeout the kernel records the failure, lets
+// its copies land and exits.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -34,34 +50,41 @@ constexpr int kTgThreads = 384;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgKStep = 64;  // elements: one 128-byte swizzle row
 
-template <int CG, int BN>
+// Epi::kSlots blocks of Epi::kSlotBytes per epilogue warp for its tensors.
+template <int CG, int BN, class Epi>
 struct TgCfg {
   static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_ROWS = BN / CG;
-  static constexpr int B_BYTES = B_ROWS * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 6;
+  static constexpr int B_ROWS = BN / CG;         // at most; bn / CG are used
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * 128;
+  static constexpr int EPI_BYTES = kTgEpiWarps * Epi::kSlots * Epi::kSlotBytes;
+  static constexpr int FIT = (232448 - 2048 - EPI_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES = FIT < 6 ? FIT : 6;
   static constexpr uint32_t TMEM_COLS = 2 * BN;  // two accumulators
-  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-  static constexpr int NBAR = 2 * STAGES + 5;    // full, empty, accfull[2], accempty[2], drain
+  static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
+  // full, empty, accfull[2], accempty[2], drain, one per epilogue block
+  static constexpr int NBAR = 2 * STAGES + 5 + kTgEpiWarps * Epi::kSlots;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_DYN = OFF_MISC + 16 + 1024;
   static_assert(BN == 128 || BN == 256, "BN");
+  static_assert(STAGES >= 4, "ring");
   static_assert(TMEM_COLS <= 512, "TMEM");
-  static_assert(B_ROWS % 64 == 0, "MN-major boxes hold 64 rows");
   static_assert(SMEM_DYN <= 232448, "shared memory");
 };
 
+// Operands, and the epilogue's tensors (32 x 32 boxes; unused ones are zero).
 struct TgMaps {
   CUtensorMap a, b, a_lo, b_lo;
+  CUtensorMap in, in_lo, out, out_lo;
 };
 
 struct TgShape {
   int M, N;              // output rows and columns
+  int bn;                // columns of a tile
   int steps;             // 64-k steps of the contraction
   int mt, nt;            // tiles
   int per_batch;         // tiles of one batch entry
-  int ksplit, split_steps;
+  int ksplit, split_steps;  // slices of the contraction (tiles of their own, or a cluster's CTAs)
   int tiles;             // all: batch * per_batch * ksplit
   int sym;               // only tiles with m >= n (square output)
   int group;             // m tiles that share one sweep over n
@@ -248,24 +271,197 @@ __device__ __forceinline__ void tg_load(const CUtensorMap* map, bool mn, int row
   }
 }
 
+// ------------------------------------------------------- epilogue machinery
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1,
+                                             int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(src)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// At most `n` of this thread's store groups still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // What an epilogue knows about its part of a tile.
 struct TgPart {
   TgTile tile;
-  int row;       // output row of this thread
-  int col0;      // first output column of this warp
-  uint32_t tmem; // address of that column for this warp's lanes
-  int half;      // column half
+  int row0, row;        // first output row of the warp, row of this thread
+  int col0, col_end;    // the tile's columns [col0, col_end)
+  int first, step;      // the warp's chunks: columns col0 + first + i * step, 32 each
+  bool dry;             // an empty pass: no tensor is read or written
+  bool live;            // this thread's row exists (never in a dry pass)
+
+  __device__ __forceinline__ int chunks() const {
+    const int w = col_end - col0 - first;
+    return w <= 0 ? 0 : (w + step - 1) / step;
+  }
+};
+
+// A warp's blocks of shared memory, used in turn; `seq` counts blocks.
+// 16-bit tensors: 32 rows of 64 bytes, 64-byte swizzle (16-byte piece j of
+// row r at piece j ^ ((r >> 1) & 3)); fp32: 32 rows of 128 bytes, 128-byte
+// swizzle (piece j at j ^ (r & 7)).  Either way the lanes of a quarter warp,
+// one row each, hit all banks once.
+struct TgStage {
+  uint8_t* base;
+  uint64_t* bars;
+  uint32_t seq;
+  int lane;
+  volatile int* abort_flag;
+  int* status;
+  uint64_t limit;
+};
+
+__device__ __forceinline__ uint32_t block16_piece(int lane, int j) {
+  return static_cast<uint32_t>(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint32_t block32_piece(int lane, int j) {
+  return static_cast<uint32_t>(lane * 128 + ((j ^ (lane & 7)) << 4));
+}
+
+__device__ __forceinline__ void block16_write(uint8_t* blk, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(blk + block16_piece(lane, j)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+__device__ __forceinline__ void block16_read(const uint8_t* blk, int lane, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = *reinterpret_cast<const uint4*>(blk + block16_piece(lane, j));
+    w[4 * j] = v.x;
+    w[4 * j + 1] = v.y;
+    w[4 * j + 2] = v.z;
+    w[4 * j + 3] = v.w;
+  }
+}
+
+// Loads of the epilogue's input blocks, two chunks ahead, for an Epi with
+// three slots whose outputs replace the inputs in place.
+template <class Epi>
+struct TgInput {
+  // Chunk i of the part into the slot of block seq + i.
+  static __device__ __forceinline__ void issue(TgStage& st, const TgMaps& m, const TgPart& t,
+                                               int i, uint32_t seq, bool two, uint32_t bytes) {
+    const uint32_t s = seq % Epi::kSlots;
+    uint8_t* blk = st.base + s * Epi::kSlotBytes;
+    const int col = t.col0 + t.first + i * t.step;
+    mbar_arrive_expect_tx(&st.bars[s], two ? 2 * bytes : bytes);
+    const uint32_t bar = smem_u32(&st.bars[s]);
+    tg_tma_load<1>(smem_u32(blk), &m.in, col, t.row0, t.tile.b, bar);
+    if (two) tg_tma_load<1>(smem_u32(blk + bytes), &m.in_lo, col, t.row0, t.tile.b, bar);
+  }
+  static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const TgPart& t,
+                                               bool two, uint32_t bytes) {
+    if (st.lane == 0 && !t.dry) {
+      bulk_wait_read<0>();
+      const int n = t.chunks();
+      if (n > 0) issue(st, m, t, 0, st.seq, two, bytes);
+      if (n > 1) issue(st, m, t, 1, st.seq + 1, two, bytes);
+    }
+  }
+  // Wait for the current block; on a timeout also for the one behind it.
+  static __device__ __forceinline__ bool wait(TgStage& st, const TgPart& t, int i) {
+    if (t.dry) return true;
+    const uint32_t s = st.seq % Epi::kSlots, ph = (st.seq / Epi::kSlots) & 1u;
+    if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&st.bars[s], ph, nullptr, st.limit)))
+      return true;
+    *st.abort_flag = 1;
+    if (st.lane == 0) {
+      record_failure(st.status, DEV_TIMEOUT_EPILOGUE);
+      if (i + 1 < t.chunks()) {
+        const uint32_t s1 = (st.seq + 1) % Epi::kSlots, p1 = ((st.seq + 1) / Epi::kSlots) & 1u;
+        if (!mbar_wait_bounded(&st.bars[s1], p1, nullptr, st.limit))
+          record_failure(st.status, DEV_TIMEOUT_DRAIN);
+      }
+    }
+    __syncwarp();
+    return false;
+  }
+  // Loads that begin() issued for a part that is not run.
+  static __device__ __forceinline__ void abandon(TgStage& st, const TgPart& t) {
+    if (st.lane != 0) return;
+    for (int i = 0; i < 2 && i < t.chunks(); ++i) {
+      const uint32_t s = (st.seq + i) % Epi::kSlots, ph = ((st.seq + i) / Epi::kSlots) & 1u;
+      if (!mbar_wait_bounded(&st.bars[s], ph, nullptr, st.limit))
+        record_failure(st.status, DEV_TIMEOUT_DRAIN);
+    }
+  }
+  // After the store of chunk i was committed: fetch chunk i + 2 into the slot
+  // that the store before it has finished reading.
+  static __device__ __forceinline__ void next(TgStage& st, const TgMaps& m, const TgPart& t,
+                                              int i, bool two, uint32_t bytes) {
+    if (st.lane == 0 && !t.dry && i + 2 < t.chunks()) {
+      bulk_wait_read<1>();
+      issue(st, m, t, i + 2, st.seq + 2, two, bytes);
+    }
+    ++st.seq;
+  }
+};
+
+// The block for the next output of an Epi with two slots and no inputs.
+template <class Epi>
+__device__ __forceinline__ uint8_t* tg_out_block(TgStage& st) {
+  if (st.lane == 0) bulk_wait_read<1>();
+  __syncwarp();
+  return st.base + (st.seq++ % Epi::kSlots) * Epi::kSlotBytes;
+}
+
+// Accumulator values of this thread's row, 32 columns from column c of the
+// tile: from TMEM, or the sum over the CTAs of a cluster.
+struct TgTmemSrc {
+  uint32_t addr;
+  __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
+    tmem_ld_32x32b_x32(addr + c, r);
+    tmem_ld_wait();
+  }
+};
+
+template <int SPLIT>
+struct TgClusterSrc {
+  uint32_t addr[SPLIT];  // of this thread's row in each CTA's [column][128] fp32 part
+  __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
+#pragma unroll
+    for (int s = 0; s < SPLIT; ++s) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float v;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(v)
+                     : "r"(addr[s] + static_cast<uint32_t>((c + i) * 512)));
+        r[i] = s == 0 ? __float_as_uint(v) : __float_as_uint(__fadd_rn(__uint_as_float(r[i]), v));
+      }
+    }
+  }
 };
 
 // ------------------------------------------------------------------- kernel
 
-// Epi: struct with Params and template<int COLS> run(const Params&, const
-// TgShape&, const TgPart&), which reads COLS columns of the warp's lanes.
-template <int CG, int BN, class Epi>
+// Epi: struct with Params, kSlots, kSlotBytes, begin(...) (called before the
+// accumulator is waited for), run(...), which takes the part's chunks, and
+// abandon(...) for a part that was begun and is not run.
+template <int CG, int BN, int SPLIT, class Epi>
 __global__ void __launch_bounds__(kTgThreads, 1)
 tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
                const typename Epi::Params ep) {
-  using C = TgCfg<CG, BN>;
+  using C = TgCfg<CG, BN, Epi>;
+  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::OFF_EPI >= 65536), "split");
   extern __shared__ uint8_t tg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(tg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -274,13 +470,18 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   uint64_t* accfull = empty + C::STAGES;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
+  uint64_t* epi_bars = drain + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  constexpr int CLUSTER = CG * SPLIT;
+  const uint32_t rank = CLUSTER > 1 ? cluster_rank() : 0u;
+  const uint32_t half_rank = CG == 2 ? rank : 0u;  // which half of the pair's tile
   const uint64_t limit = p.wait_limit_ns;
-  const int worker = static_cast<int>(blockIdx.x) / CG;
-  const int workers = static_cast<int>(gridDim.x) / CG;
+  const int worker = static_cast<int>(blockIdx.x) / CLUSTER;
+  const int workers = static_cast<int>(gridDim.x) / CLUSTER;
+  const int b_rows = p.bn / CG;
+  const uint32_t stage_tx = static_cast<uint32_t>(CG * (C::A_BYTES + b_rows * 128));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -292,30 +493,69 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       mbar_init(&accempty[i], CG * kTgEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < kTgEpiWarps * Epi::kSlots; ++i) mbar_init(&epi_bars[i], 1);
     *abort_flag = 0;
     fence_mbarrier_init();
+  }
+  if (warp == 1 && lane == 0) {
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
+    if (p.passes == 3) {
+      tma_prefetch_desc(&maps.a_lo);
+      tma_prefetch_desc(&maps.b_lo);
+    }
   }
   if (warp == 2) tg_tmem_alloc<CG>(tmem_slot, C::TMEM_COLS);
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  if constexpr (CLUSTER > 1) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
 
+  // Contraction steps of a tile that this CTA (or pair) takes.
+  auto k_range = [&](const TgTile& tile, int& lo, int& hi) {
+    const int slice = SPLIT > 1 ? static_cast<int>(rank) : tile.split;
+    lo = slice * p.split_steps;
+    hi = min(p.steps, lo + p.split_steps);
+  };
+  auto part_of = [&](const TgTile& tile, int q, int half) {
+    TgPart t;
+    t.tile = tile;
+    t.row0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank) + 32 * q;
+    t.row = t.row0 + lane;
+    t.col0 = tile.n * p.bn;
+    t.col_end = min(p.N, t.col0 + p.bn);
+    t.first = 32 * half;
+    t.step = 64;
+    t.dry = false;
+    t.live = t.row < p.M;
+    return t;
+  };
+  const int q = warp & 3, half = (warp - 4) >> 2;
+  TgStage st;
+  st.base = smem + C::OFF_EPI + (warp - 4) * Epi::kSlots * Epi::kSlotBytes;
+  st.bars = epi_bars + (warp - 4) * Epi::kSlots;
+  st.seq = 0;
+  st.lane = lane;
+  st.abort_flag = abort_flag;
+  st.status = p.status;
+  st.limit = limit;
+  const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+
+  if (warp < 4) {
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+  }
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;  // stages issued
       bool ok = true;
       for (int t = worker; t < p.tiles && ok; t += workers) {
         const TgTile tile = tg_tile(p, t);
-        const int k_lo = tile.split * p.split_steps;
-        const int k_hi = min(p.steps, k_lo + p.split_steps);
-        const int a0 = tile.m * 128 * CG + 128 * static_cast<int>(rank);
-        const int b0 = tile.n * BN + C::B_ROWS * static_cast<int>(rank);
+        int k_lo, k_hi;
+        k_range(tile, k_lo, k_hi);
+        const int a0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank);
+        const int b0 = tile.n * p.bn + b_rows * static_cast<int>(half_rank);
         for (int pass = 0; pass < p.passes && ok; ++pass) {
           const CUtensorMap* ma = pass == 2 ? &maps.a_lo : &maps.a;
           const CUtensorMap* mb = pass == 1 ? &maps.b_lo : &maps.b;
@@ -330,9 +570,9 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
             const uint32_t dst = smem_u32(smem + s * C::STAGE_BYTES);
             uint32_t bar = smem_u32(&full[s]);
             if (CG == 2) bar = map_to_rank(bar, 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::STAGE_BYTES);
+            if (half_rank == 0) mbar_arrive_expect_tx(&full[s], stage_tx);
             tg_load<CG>(ma, p.a_mn, 128, dst, a0, j * kTgKStep, tile.b, bar);
-            tg_load<CG>(mb, p.b_mn, C::B_ROWS, dst + C::A_BYTES, b0, j * kTgKStep, tile.b, bar);
+            tg_load<CG>(mb, p.b_mn, b_rows, dst + C::A_BYTES, b0, j * kTgKStep, tile.b, bar);
           }
         }
       }
@@ -346,21 +586,20 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         }
       // After a timeout, let the copies in flight land first (otherwise the
       // MMAs have consumed them all).
-      if (*abort_flag && rank == 0)
+      if (*abort_flag && half_rank == 0)
         for (uint32_t i = from; i < it; ++i)
           if (!mbar_wait_bounded(&full[i % C::STAGES], (i / C::STAGES) & 1u, nullptr, limit))
             record_failure(p.status, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (lane == 0 && half_rank == 0) {
       uint32_t it = 0;
       int local = 0;
       bool ok = true;
       for (int t = worker; t < p.tiles && ok; t += workers, ++local) {
         const int buf = local & 1;
-        const TgTile tile = tg_tile(p, t);
-        const int k_lo = tile.split * p.split_steps;
-        const int k_hi = min(p.steps, k_lo + p.split_steps);
+        int k_lo, k_hi;
+        k_range(tg_tile(p, t), k_lo, k_hi);
         const int n_it = (k_hi - k_lo) * p.passes;
         if (local >= 2 && !mbar_wait_bounded(&accempty[buf],
                                              static_cast<uint32_t>((local >> 1) - 1) & 1u,
@@ -401,27 +640,53 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       }
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    {
+      TgPart t = part_of(TgTile{0, 0, 0, 0}, q, half);
+      t.dry = true;
+      t.live = false;
+      t.first = 0;
+      t.col_end = min(t.col_end, 32);
+      if constexpr (SPLIT == 1) {
+        Epi::run(ep, p, maps, t, st, TgTmemSrc{lanes});
+      } else {
+        TgClusterSrc<SPLIT> src;
+#pragma unroll
+        for (int s = 0; s < SPLIT; ++s) src.addr[s] = map_to_rank(smem_u32(smem), rank);
+        Epi::run(ep, p, maps, t, st, src);
+      }
+      st.seq = 0;
+    }
+    pdl_wait_prior_grid();
     int local = 0;
     for (int t = worker; t < p.tiles; t += workers, ++local) {
       const int buf = local & 1;
+      const TgPart part = part_of(tg_tile(p, t), q, half);
+      if constexpr (SPLIT == 1) Epi::begin(st, maps, ep, part);
       const bool ok = __all_sync(
           0xFFFFFFFFu, mbar_wait_bounded(&accfull[buf], static_cast<uint32_t>(local >> 1) & 1u,
                                          abort_flag, limit));
       if (!ok) {
         *abort_flag = 1;
         if (lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
+        if constexpr (SPLIT == 1) Epi::abandon(st, ep, part);
         break;
       }
       tc_fence_after_sync();
-      TgPart part;
-      part.tile = tg_tile(p, t);
-      part.row = part.tile.m * 128 * CG + 128 * static_cast<int>(rank) + 32 * q + lane;
-      part.col0 = part.tile.n * BN + half * (BN / 2);
-      part.tmem = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                  static_cast<uint32_t>(buf * BN + half * (BN / 2));
-      part.half = half;
-      Epi::template run<BN / 2>(ep, p, part);
+      const uint32_t acc = lanes + static_cast<uint32_t>(buf * BN);
+      if constexpr (SPLIT == 1) {
+        Epi::run(ep, p, maps, part, st, TgTmemSrc{acc});
+      } else {
+        // This CTA's part, [column][row] fp32, over the ring (all consumed).
+        float* part_sum = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+        for (int c = 32 * half; c < BN; c += 64) {
+          uint32_t r[32];
+          TgTmemSrc{acc}.load(c, r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            part_sum[(c + i) * 128 + 32 * q + lane] = __uint_as_float(r[i]);
+        }
+      }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -433,9 +698,30 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
     }
   }
   __syncwarp();
+  if constexpr (SPLIT > 1) {
+    // One tile per cluster: its parts meet, and CTA r finishes columns
+    // [128 r / SPLIT, 128 (r + 1) / SPLIT), a chunk of 32 per warp.
+    __syncthreads();
+    cluster_sync();
+    constexpr int kChunks = 4 / SPLIT;
+    if (warp >= 4 && half < kChunks && *abort_flag == 0) {
+      TgPart part = part_of(tg_tile(p, worker), q, half);
+      part.first = 32 * (static_cast<int>(rank) * kChunks + half);
+      part.step = 1 << 20;
+      TgClusterSrc<SPLIT> src;
+#pragma unroll
+      for (int s = 0; s < SPLIT; ++s)
+        src.addr[s] = map_to_rank(smem_u32(smem), s) + static_cast<uint32_t>(4 * (32 * q + lane));
+      Epi::begin(st, maps, ep, part);
+      Epi::run(ep, p, maps, part, st, src);
+    }
+    __syncwarp();
+  }
+  if (warp >= 4 && lane == 0) bulk_wait_all();
+  __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  if constexpr (CLUSTER > 1) cluster_sync();
   if (warp == 2) {
     tc_fence_after_sync();
     tg_tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
@@ -444,88 +730,119 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
 
 // ------------------------------------------------------------ epilogue tools
 
-// Store 32 consecutive 16-bit values of one row (two per word); vec when the
-// address is 16-byte aligned and all 32 fit, else n of them one by one.
-__device__ __forceinline__ void store_row32_16(uint16_t* dst, const uint32_t (&w)[16], bool vec,
-                                               int n) {
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(dst)[i] =
-          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-  }
-}
-
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(a))) |
          (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(b))) << 16);
 }
 
-// D to memory: fp32 (plus `add` when given; the part's own slice for a split
-// contraction) or bf16.
-struct TgStore {
+// Store a chunk's block and count it as one group of this warp.
+__device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensorMap* map,
+                                               const uint8_t* blk, int col, const TgPart& t) {
+  if (st.lane == 0 && !t.dry) tma_store_3d(map, smem_u32(blk), col, t.row0, t.tile.b);
+}
+
+// D to bf16, times a device scalar when given.
+struct TgStoreBf16 {
+  static constexpr int kSlots = 2, kSlotBytes = 2048;
   struct Params {
-    float* f32;           // fp32 out, or
-    __nv_bfloat16* bf16;  // bf16 out
-    const float* add;     // fp32 [M][ld] added first, or null
-    int64_t ld;           // of f32 and add
-    int64_t ld_out;       // of bf16
-    int64_t split_stride; // elements between the slices of a split contraction
-    const float* scale;   // device scalar times the bf16 result, or null
+    const float* scale;
   };
-  template <int COLS>
-  static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgPart& t) {
+  static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
+                                               const TgPart&) {}
+  static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape&, const TgMaps& m,
+                                             const TgPart& t, TgStage& st, Src src) {
+    const float f = e.scale && !t.dry ? __ldcg(e.scale) : 1.0f;
+    const int n = t.chunks();
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      const int col = t.col0 + c;
-      if (col >= p.N) break;  // the same for all of the warp
+    for (int i = 0; i < n; ++i) {
+      const int c = t.first + i * t.step;
+      uint32_t r[32], w[16];
+      src.load(c, r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * f, __uint_as_float(r[2 * j + 1]) * f);
+      uint8_t* blk = tg_out_block<TgStoreBf16>(st);
+      block16_write(blk, st.lane, w);
+      fence_proxy_async_smem();
+      __syncwarp();
+      tg_store_block(st, &m.out, blk, t.col0 + c, t);
+      if (st.lane == 0) bulk_commit();
+    }
+  }
+};
+
+// D (+ an fp32 tensor) to fp32, or times a device scalar to bf16; a slice of
+// a split contraction goes to its own [M][N] of the output.
+struct TgAccumulate {
+  static constexpr int kSlots = 3, kSlotBytes = 4096;
+  struct Params {
+    int add;             // add `in`
+    int to_bf16;         // `out` is bf16 (else fp32)
+    const float* scale;  // for bf16
+  };
+  using In = TgInput<TgAccumulate>;
+  static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
+                                               const TgPart& t) {
+    if (e.add)
+      In::begin(st, m, t, false, 4096);
+    else if (st.lane == 0)
+      bulk_wait_read<0>();
+    __syncwarp();
+  }
+  static __device__ __forceinline__ void abandon(TgStage& st, const Params& e, const TgPart& t) {
+    if (e.add) In::abandon(st, t);
+  }
+  template <class Src>
+  static __device__ __forceinline__ void run(const Params& e, const TgShape&, const TgMaps& m,
+                                             const TgPart& t, TgStage& st, Src src) {
+    const float f = e.to_bf16 && !t.dry ? __ldcg(e.scale) : 1.0f;
+    TgPart o = t;             // slices are the output's batch entries
+    o.tile.b = t.tile.split;
+    const int n = t.chunks();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int c = t.first + i * t.step;
+      uint8_t* blk = st.base + (st.seq % kSlots) * kSlotBytes;
+      if (e.add && !In::wait(st, t, i)) break;
       uint32_t r[32];
-      tmem_ld_32x32b_x32(t.tmem + c, r);
-      tmem_ld_wait();
-      if (t.row < p.M) {
-        const int n = min(32, p.N - col);
-        if (e.add) {
-          const float* s = e.add + t.row * e.ld + col;
-          if (n == 32 && (e.ld & 3) == 0) {
+      src.load(c, r);
+      if (e.add) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 v = *reinterpret_cast<const float4*>(s + 4 * i);
-              r[4 * i] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i]), v.x));
-              r[4 * i + 1] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i + 1]), v.y));
-              r[4 * i + 2] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i + 2]), v.z));
-              r[4 * i + 3] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i + 3]), v.w));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n) r[i] = __float_as_uint(__fadd_rn(__uint_as_float(r[i]), s[i]));
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(blk + block32_piece(st.lane, j));
+          r[4 * j] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * j]), v.x));
+          r[4 * j + 1] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * j + 1]), v.y));
+          r[4 * j + 2] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * j + 2]), v.z));
+          r[4 * j + 3] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * j + 3]), v.w));
         }
-        if (e.bf16) {
-          uint32_t w[16];
-          const float f = e.scale ? __ldg(e.scale) : 1.0f;
+      }
+      if (e.to_bf16) {
+        uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = pack_bf16x2(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
-          store_row32_16(reinterpret_cast<uint16_t*>(e.bf16) + t.row * e.ld_out + col, w,
-                         n == 32 && (e.ld_out & 7) == 0, n);
-        } else {
-          float* d = e.f32 + t.tile.split * e.split_stride + t.row * e.ld + col;
-          if (n == 32 && (e.ld & 3) == 0) {
+        for (int j = 0; j < 16; ++j)
+          w[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * f, __uint_as_float(r[2 * j + 1]) * f);
+        __syncwarp();  // the whole block was read
+        block16_write(blk, st.lane, w);
+      } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(d)[i] =
-                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n) d[i] = __uint_as_float(r[i]);
-          }
-        }
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(blk + block32_piece(st.lane, j)) =
+              make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      tg_store_block(st, &m.out, blk, t.col0 + c, o);
+      if (st.lane == 0) {
+        bulk_commit();
+        if (!e.add) bulk_wait_read<2>();  // the next block's slot is free again
+      }
+      if (e.add) {
+        In::next(st, m, t, i, false, 4096);
+      } else {
+        ++st.seq;
+        __syncwarp();
       }
     }
   }

@@ -25,37 +25,71 @@ struct TgOperand {
   bool mn = false;
 };
 
+// A tensor of the epilogue: [batch][M][N] with row stride ld.
+struct TgTensor {
+  const void* p = nullptr;
+  const void* lo = nullptr;
+  int64_t ld = 0, batch_stride = 0, batch = 1;
+  CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+};
+
+// How a product is cut: SM pairs on 256-row tiles (cg = 2) or single SMs on
+// 128-row ones, bn columns a tile, and the CTAs of a cluster that share one
+// tile's contraction.
+struct TgPlan {
+  int cg = 1, bn = 128, split = 1;
+};
+
 struct TgProblem {
   TgOperand a, b;
+  TgTensor in, out;
   int64_t M = 0, N = 0, Kc = 0, batch = 1;
   bool bf16 = true;
   bool sym = false;
   int passes = 1;
-  int ksplit = 1;
+  int ksplit = 1;            // slices of the contraction as tiles of their own
+  TgPlan plan;
 };
 
-// 3-D tensor [batch][rows][inner] of 16-bit elements, boxes of 64 x box_rows,
-// 128-byte swizzle; out-of-range elements read as zero.
-bool make_tmap_16(CUtensorMap* map, const void* base, bool bf16, int64_t inner, int64_t rows,
-                  int64_t batch, int64_t ld, int64_t batch_stride, int box_rows) {
+// 3-D tensor [batch][rows][inner], boxes of box_inner x box_rows;
+// out-of-range elements read as zero and are not written.
+bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, int64_t inner,
+                  int64_t rows, int64_t batch, int64_t ld, int64_t batch_stride, int box_inner,
+                  int box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
+  const int64_t size = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(batch)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * ld),
-                           static_cast<cuuint64_t>(2 * (batch > 1 ? batch_stride : ld * rows))};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(size * ld),
+                           static_cast<cuuint64_t>(size * (batch > 1 ? batch_stride : ld * rows))};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_operand_map(CUtensorMap* map, const TgOperand& o, const void* base, bool bf16,
                       int64_t rows, int64_t Kc, int64_t batch, int tile_rows) {
-  return o.mn ? make_tmap_16(map, base, bf16, rows, Kc, batch, o.ld, o.batch_stride, 64)
-              : make_tmap_16(map, base, bf16, Kc, rows, batch, o.ld, o.batch_stride, tile_rows);
+  const CUtensorMapDataType type =
+      bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return o.mn ? make_tmap_3d(map, base, type, rows, Kc, batch, o.ld, o.batch_stride, 64, 64,
+                             CU_TENSOR_MAP_SWIZZLE_128B)
+              : make_tmap_3d(map, base, type, Kc, rows, batch, o.ld, o.batch_stride, 64,
+                             tile_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// 32 x 32 blocks: rows of 64 bytes (16-bit) or 128 bytes (fp32).
+bool make_tensor_maps(CUtensorMap* map, CUtensorMap* map_lo, const TgTensor& t, int64_t M,
+                      int64_t N) {
+  const CUtensorMapSwizzle swz = t.type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : CU_TENSOR_MAP_SWIZZLE_64B;
+  return (!t.p || make_tmap_3d(map, t.p, t.type, N, M, t.batch, t.ld, t.batch_stride, 32, 32,
+                               swz)) &&
+         (!t.lo || make_tmap_3d(map_lo, t.lo, t.type, N, M, t.batch, t.ld, t.batch_stride, 32, 32,
+                                swz));
 }
 
 int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) {
@@ -63,28 +97,49 @@ int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) 
   return batch * (sym ? mt * (mt + 1) / 2 : mt * nt);
 }
 
-// Whether a product takes 256 x 256 tiles on SM pairs rather than 128 x 128
-// tiles: whichever needs less time for its waves of tiles, a 256-tile's step
-// costing a pair twice a 128-tile's step on one SM, and the small tile's
-// step, which reads twice the shared memory per MMA, 1.3 times its share.
-bool tg_use_pairs(int64_t M, int64_t N, int64_t batch, bool sym) {
-  const int64_t t2 = tg_tiles(M, N, batch, sym, 256, 256);
-  const int64_t t1 = tg_tiles(M, N, batch, sym, 128, 128);
-  return 2.0 * static_cast<double>(ceil_div(t2, kPlanSms / 2)) <
-         1.3 * static_cast<double>(ceil_div(t1, kPlanSms));
+// Cycles that a plan needs, roughly: its waves of tiles, a tile's steps and
+// its epilogue.  A pair's 64-k step takes 660 cycles (measured; the MMAs
+// alone 512), a 128 x 128 step 600 (32 KiB at 64 bytes a cycle are 512; the
+// MMAs 256); the epilogue and what a launch waits for come on top of each
+// wave, and for a cluster's split the meeting of the parts.
+double tg_cost(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, const TgPlan& pl) {
+  const int64_t tiles = tg_tiles(M, N, batch, sym, 128 * pl.cg, pl.bn);
+  const double waves = static_cast<double>(ceil_div(tiles * pl.split, kPlanSms / pl.cg));
+  if (pl.cg == 2) return waves * (660.0 * static_cast<double>(steps) + 5000.0);
+  return waves * (600.0 * static_cast<double>(ceil_div(steps, pl.split)) + 3000.0 +
+                  (pl.split > 1 ? 2500.0 : 0.0));
+}
+
+// Pairs on 256 x 256 tiles, or single SMs on 128 x 128 tiles, each tile's
+// steps shared by a cluster of up to max_split CTAs: whichever tg_cost
+// prefers.  Every CTA of a cluster needs a step of its own.
+TgPlan tg_plan(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, int passes,
+               int max_split) {
+  TgPlan best{2, 256, 1};
+  double cost = tg_cost(M, N, batch, sym, steps * passes, best);
+  for (int s = 1; s <= max_split; s *= 2) {
+    const TgPlan pl{1, 128, s};
+    if ((s - 1) * ceil_div(steps, s) >= steps) continue;
+    const double c = tg_cost(M, N, batch, sym, ceil_div(steps, s) * s * passes, pl);
+    if (c < cost) {
+      cost = c;
+      best = pl;
+    }
+  }
+  return best;
 }
 
 // Resident workers (pairs or single CTAs) of one kernel instance, per device;
 // sets the kernel's shared-memory limit the first time.
-template <int CG, int BN, class Epi>
+template <int CG, int BN, int SPLIT, class Epi>
 int tg_workers(int num_sms) {
   static std::once_flag once[kMaxDevices];
   static int workers[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   std::call_once(once[dev], [dev, num_sms]() {
-    using C = TgCfg<CG, BN>;
-    auto kernel = tc_gemm_kernel<CG, BN, Epi>;
+    using C = TgCfg<CG, BN, Epi>;
+    auto kernel = tc_gemm_kernel<CG, BN, SPLIT, Epi>;
     if (!set_smem(kernel, C::SMEM_DYN)) return;
     if (CG == 1) {
       workers[dev] = num_sms;
@@ -107,41 +162,46 @@ int tg_workers(int num_sms) {
   return workers[dev];
 }
 
-template <int CG, int BN, class Epi>
+template <int CG, int BN, int SPLIT, class Epi>
 bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
                             const typename Epi::Params& ep, cudaStream_t stream) {
-  using C = TgCfg<CG, BN>;
-  const int workers = tg_workers<CG, BN, Epi>(ds.num_sms);
+  using C = TgCfg<CG, BN, Epi>;
+  const int workers = tg_workers<CG, BN, SPLIT, Epi>(ds.num_sms);
   if (workers < 1) return cuda_status(cudaErrorInvalidConfiguration);
+  const int bn = g.plan.bn, b_rows = bn / CG;
   TgMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   if (!make_operand_map(&maps.a, g.a, g.a.p, g.bf16, g.M, g.Kc, g.batch, 128) ||
-      !make_operand_map(&maps.b, g.b, g.b.p, g.bf16, g.N, g.Kc, g.batch, C::B_ROWS))
+      !make_operand_map(&maps.b, g.b, g.b.p, g.bf16, g.N, g.Kc, g.batch, b_rows) ||
+      !make_tensor_maps(&maps.in, &maps.in_lo, g.in, g.M, g.N) ||
+      !make_tensor_maps(&maps.out, &maps.out_lo, g.out, g.M, g.N))
     return BITNET_ERR_CUDA;
   if (g.passes == 3 &&
       (!make_operand_map(&maps.a_lo, g.a, g.a.lo, g.bf16, g.M, g.Kc, g.batch, 128) ||
-       !make_operand_map(&maps.b_lo, g.b, g.b.lo, g.bf16, g.N, g.Kc, g.batch, C::B_ROWS)))
+       !make_operand_map(&maps.b_lo, g.b, g.b.lo, g.bf16, g.N, g.Kc, g.batch, b_rows)))
     return BITNET_ERR_CUDA;
   TgShape p{};
   p.M = static_cast<int>(g.M);
   p.N = static_cast<int>(g.N);
+  p.bn = bn;
   p.steps = static_cast<int>(ceil_div(g.Kc, kTgKStep));
   p.mt = static_cast<int>(ceil_div(g.M, 128 * CG));
-  p.nt = static_cast<int>(ceil_div(g.N, BN));
+  p.nt = static_cast<int>(ceil_div(g.N, bn));
   p.sym = g.sym ? 1 : 0;
-  p.per_batch = static_cast<int>(tg_tiles(g.M, g.N, 1, g.sym, 128 * CG, BN));
-  p.split_steps = static_cast<int>(ceil_div(p.steps, g.ksplit));
+  p.per_batch = static_cast<int>(tg_tiles(g.M, g.N, 1, g.sym, 128 * CG, bn));
+  p.split_steps = static_cast<int>(ceil_div(p.steps, SPLIT > 1 ? SPLIT : g.ksplit));
   p.ksplit = g.ksplit;
   p.tiles = static_cast<int>(g.batch * p.per_batch * p.ksplit);
   p.group = 8;
   p.passes = g.passes;
   p.a_mn = g.a.mn ? 1 : 0;
   p.b_mn = g.b.mn ? 1 : 0;
-  p.idesc = tg_idesc(128 * CG, BN, g.bf16, g.a.mn, g.b.mn);
+  p.idesc = tg_idesc(128 * CG, bn, g.bf16, g.a.mn, g.b.mn);
   p.status = ds.status;
   p.wait_limit_ns = kWaitLimitNs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(CG * std::min(workers, p.tiles)));
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      CG * SPLIT * (SPLIT > 1 ? p.tiles : std::min(workers, p.tiles))));
   cfg.blockDim = dim3(kTgThreads);
   cfg.dynamicSmemBytes = C::SMEM_DYN;
   cfg.stream = stream;
@@ -149,19 +209,31 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = CG * SPLIT;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, tc_gemm_kernel<CG, BN, Epi>, maps, p, ep));
+  cfg.numAttrs = CG * SPLIT > 1 ? 2 : 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, tc_gemm_kernel<CG, BN, SPLIT, Epi>, maps, p, ep));
 }
 
-template <class Epi>
-bitnet_status launch_tg(const DeviceState& ds, const TgProblem& g, bool pairs,
+// Pairs of 256 columns, or single SMs with tiles of up to BN1.
+template <int BN1, class Epi>
+bitnet_status launch_tg(const DeviceState& ds, const TgProblem& g,
                         const typename Epi::Params& ep, cudaStream_t stream) {
-  return pairs ? launch_tg_cfg<2, 256, Epi>(ds, g, ep, stream)
-               : launch_tg_cfg<1, 128, Epi>(ds, g, ep, stream);
+  return g.plan.cg == 2 ? launch_tg_cfg<2, 256, 1, Epi>(ds, g, ep, stream)
+                        : launch_tg_cfg<1, BN1, 1, Epi>(ds, g, ep, stream);
+}
+
+// The same with the contraction of a 128 x 128 tile shared by a cluster.
+template <class Epi>
+bitnet_status launch_tg_split(const DeviceState& ds, const TgProblem& g,
+                              const typename Epi::Params& ep, cudaStream_t stream) {
+  switch (g.plan.split) {
+    case 2: return launch_tg_cfg<1, 128, 2, Epi>(ds, g, ep, stream);
+    case 4: return launch_tg_cfg<1, 128, 4, Epi>(ds, g, ep, stream);
+    default: return launch_tg<128, Epi>(ds, g, ep, stream);
+  }
 }
 
 template <typename... KArgs, typename... Args>
@@ -190,22 +262,30 @@ bitnet_status check_ce_shape(int64_t M, int64_t V, int64_t K) {
   return BITNET_OK;
 }
 
+// The logits' product, x [M] by `cols` of W.  Up to 128 tokens it reads W
+// once and that is its time: single SMs, and tiles as wide as spreads the
+// columns evenly over all of them (a multiple of `unit`).
+TgPlan ce_logits_plan(int64_t M, int64_t cols, int64_t K, int unit) {
+  if (M > 128) {
+    const TgPlan pl = tg_plan(M, cols, 1, false, ceil_div(K, kTgKStep), 1, 1);
+    return pl;
+  }
+  const int64_t rounds = ceil_div(cols, 256LL * kPlanSms);
+  return TgPlan{1, static_cast<int>(round_up(ceil_div(cols, rounds * kPlanSms), unit)), 1};
+}
+
 struct CeFwdLayout {
-  bool pairs;
+  TgPlan plan;
   int64_t parts;
-  size_t part, logit, total;
+  size_t part, total;
 };
 
-CeFwdLayout ce_fwd_layout(int64_t M, int64_t V) {
+CeFwdLayout ce_fwd_layout(int64_t M, int64_t V, int64_t K) {
   CeFwdLayout w{};
-  w.pairs = tg_use_pairs(M, V, 1, false);
-  w.parts = 2 * ceil_div(V, w.pairs ? 256 : 128);
-  size_t o = 0;
-  w.part = o;
-  o = align256(o + static_cast<size_t>(8 * w.parts * M));
-  w.logit = o;
-  o = align256(o + static_cast<size_t>(4 * M));
-  w.total = o;
+  w.plan = ce_logits_plan(M, V, K, 16);
+  w.parts = 2 * ceil_div(V, w.plan.bn);
+  w.part = 0;
+  w.total = align256(static_cast<size_t>(8 * w.parts * M));
   return w;
 }
 
@@ -214,9 +294,9 @@ constexpr int64_t kCePieceBytes = 256LL << 20;
 
 struct CeBwdLayout {
   int64_t cols, pieces;      // vocabulary columns of a piece, number of pieces
-  bool dx_pairs;
+  TgPlan dx_plan;
   int dx_split;
-  size_t g, acc, part, scale, total;
+  size_t g, acc, part, logit, scale, total;
 };
 
 CeBwdLayout ce_bwd_layout(int64_t M, int64_t V, int64_t K) {
@@ -227,10 +307,9 @@ CeBwdLayout ce_bwd_layout(int64_t M, int64_t V, int64_t K) {
   w.pieces = ceil_div(V, w.cols);
   // dx has few tiles and a long contraction: split it so that the last wave
   // of tiles is full (at most 16 slices, 4 steps each at least).
-  w.dx_pairs = M > 128 && K > 128;
-  const int64_t tiles = w.dx_pairs ? tg_tiles(M, K, 1, false, 256, 256)
-                                   : tg_tiles(M, K, 1, false, 128, 128);
-  const int64_t slots = w.dx_pairs ? kPlanSms / 2 : kPlanSms;
+  w.dx_plan = M > 128 && K > 128 ? TgPlan{2, 256, 1} : TgPlan{1, 128, 1};
+  const int64_t tiles = tg_tiles(M, K, 1, false, 128 * w.dx_plan.cg, w.dx_plan.bn);
+  const int64_t slots = kPlanSms / w.dx_plan.cg;
   const int64_t steps = ceil_div(std::min(w.cols, V), kTgKStep);
   w.dx_split = 1;
   double best = static_cast<double>(ceil_div(tiles, slots));
@@ -245,14 +324,16 @@ CeBwdLayout ce_bwd_layout(int64_t M, int64_t V, int64_t K) {
   const int64_t per = ceil_div(steps, w.dx_split);
   w.dx_split = static_cast<int>(ceil_div(steps, per));
   size_t o = 0;
-  w.g = o;
-  o = align256(o + static_cast<size_t>(2 * M * w.cols));
-  w.acc = o;
-  if (w.pieces > 1) o = align256(o + static_cast<size_t>(4 * M * K));
-  w.part = o;
-  if (w.dx_split > 1) o = align256(o + static_cast<size_t>(4 * M * K * w.dx_split));
-  w.scale = o;
-  o = align256(o + 4);
+  auto take = [&o](int64_t bytes) {
+    const size_t at = o;
+    o = align256(o + static_cast<size_t>(bytes));
+    return at;
+  };
+  w.g = take(2 * M * w.cols);
+  w.acc = take(w.pieces > 1 ? 4 * M * K : 0);
+  w.part = take(w.dx_split > 1 ? 4 * M * K * w.dx_split : 0);
+  w.logit = take(4 * M);
+  w.scale = take(4);
   w.total = o;
   return w;
 }
@@ -354,7 +435,7 @@ extern "C" {
 
 BITNET_API size_t bitnet_cross_entropy_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
   if (check_ce_shape(M, V, K) != BITNET_OK || M == 0) return 0;
-  return ce_fwd_layout(M, V).total;
+  return ce_fwd_layout(M, V, K).total;
 }
 
 BITNET_API bitnet_status bitnet_cross_entropy_forward(const void* x, const void* W,
@@ -370,7 +451,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_forward(const void* x, const void*
   if (!aligned(x, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(loss, 4) ||
       !aligned(lse, 4))
     return BITNET_ERR_MISALIGNED;
-  const CeFwdLayout L = ce_fwd_layout(M, V);
+  const CeFwdLayout L = ce_fwd_layout(M, V, K);
   if (!workspace || workspace_bytes < L.total) return BITNET_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BITNET_ERR_MISALIGNED;
   DeviceState* ds = device_state();
@@ -385,12 +466,13 @@ BITNET_API bitnet_status bitnet_cross_entropy_forward(const void* x, const void*
   g.M = M;
   g.N = V;
   g.Kc = K;
-  CeStats::Params ep{targets, reinterpret_cast<float2*>(ws + L.part),
-                     reinterpret_cast<float*>(ws + L.logit)};
-  st = launch_tg<CeStats>(*ds, g, L.pairs, ep, s);
+  g.plan = L.plan;
+  CeStats::Params ep{targets, reinterpret_cast<float2*>(ws + L.part)};
+  st = launch_tg<256, CeStats>(*ds, g, ep, s);
   if (st != BITNET_OK) return st;
   return launch_pdl(ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(M, 32))), 1024, s, ep.part,
-                    static_cast<int>(L.parts), ep.target_logit, targets, V, static_cast<int>(M),
+                    static_cast<int>(L.parts), static_cast<const __nv_bfloat16*>(x),
+                    static_cast<const __nv_bfloat16*>(W), targets, V, K, static_cast<int>(M),
                     loss, lse);
 }
 
@@ -428,7 +510,10 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
   float* acc = reinterpret_cast<float*>(ws + L.acc);
   float* part = reinterpret_cast<float*>(ws + L.part);
   float* scale = reinterpret_cast<float*>(ws + L.scale);
-  st = launch_pdl(ce_scale_kernel, dim3(1), 1024, s, dloss, targets, V, M, scale);
+  float* logit = reinterpret_cast<float*>(ws + L.logit);
+  st = launch_pdl(ce_target_kernel, dim3(static_cast<unsigned>(ceil_div(M, 8))), 256, s,
+                  static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(W),
+                  targets, dloss, M, V, K, logit, scale);
   if (st != BITNET_OK) return st;
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.cols, cols = std::min(L.cols, V - v0);
@@ -439,11 +524,14 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.a.ld = K;
       g.b.p = Wi;
       g.b.ld = K;
+      g.out.p = gbuf;
+      g.out.ld = L.cols;
       g.M = M;
       g.N = cols;
       g.Kc = K;
-      CeGrad::Params ep{targets, lse, dloss, scale, V, v0, gbuf, L.cols};
-      st = launch_tg<CeGrad>(*ds, g, tg_use_pairs(M, cols, 1, false), ep, s);
+      g.plan = ce_logits_plan(M, cols, K, 32);
+      CeGrad::Params ep{targets, lse, dloss, logit, scale, V, v0};
+      st = launch_tg<256, CeGrad>(*ds, g, ep, s);
       if (st != BITNET_OK) return st;
     }
     if (dx) {  // dx (+)= g W_i
@@ -457,22 +545,33 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.M = M;
       g.N = K;
       g.Kc = cols;
+      g.plan = L.dx_plan;
       const int64_t steps = ceil_div(cols, kTgKStep);
       const int64_t per = ceil_div(steps, L.dx_split);
       g.ksplit = static_cast<int>(ceil_div(steps, per));
-      TgStore::Params ep{};
-      ep.scale = scale;
-      ep.ld = K;
+      TgAccumulate::Params ep{};
+      g.out.ld = K;
+      g.out.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
       if (g.ksplit > 1) {
-        ep.f32 = part;
-        ep.split_stride = M * K;
+        g.out.p = part;
+        g.out.batch = g.ksplit;
+        g.out.batch_stride = M * K;
       } else {
-        ep.add = first ? nullptr : acc;
-        ep.f32 = acc;
-        ep.bf16 = last ? static_cast<__nv_bfloat16*>(dx) : nullptr;
-        ep.ld_out = K;
+        if (!first) {
+          ep.add = 1;
+          g.in.p = acc;
+          g.in.ld = K;
+          g.in.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+        }
+        g.out.p = acc;
+        if (last) {
+          ep.to_bf16 = 1;
+          ep.scale = scale;
+          g.out.p = dx;
+          g.out.type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        }
       }
-      st = launch_tg<TgStore>(*ds, g, L.dx_pairs, ep, s);
+      st = launch_tg<128, TgAccumulate>(*ds, g, ep, s);
       if (st != BITNET_OK) return st;
       if (g.ksplit > 1) {
         const int64_t n4 = M * K / 4;
@@ -491,14 +590,13 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.b.p = x;
       g.b.ld = K;
       g.b.mn = true;
+      g.out.p = static_cast<__nv_bfloat16*>(dW) + v0 * K;
+      g.out.ld = K;
       g.M = cols;
       g.N = K;
       g.Kc = M;
-      TgStore::Params ep{};
-      ep.scale = scale;
-      ep.bf16 = static_cast<__nv_bfloat16*>(dW) + v0 * K;
-      ep.ld_out = K;
-      st = launch_tg<TgStore>(*ds, g, tg_use_pairs(cols, K, 1, false), ep, s);
+      g.plan = tg_plan(cols, K, 1, false, ceil_div(M, kTgKStep), 1, 1);
+      st = launch_tg<128, TgStoreBf16>(*ds, g, TgStoreBf16::Params{scale}, s);
       if (st != BITNET_OK) return st;
     }
   }
@@ -562,8 +660,13 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
                   L.ldx, xb);
   if (st != BITNET_OK) return st;
 
-  const bool sym_pairs = tg_use_pairs(L.n, L.n, B, true);
-  const bool x_pairs = tg_use_pairs(L.n, L.k, B, false);
+  const int passes = L.split ? 3 : 1;
+  const int64_t n_steps = ceil_div(L.n, kTgKStep), k_steps = ceil_div(L.k, kTgKStep);
+  const TgPlan gram_plan = tg_plan(L.n, L.n, B, true, k_steps, passes, 4);
+  const TgPlan poly_plan = tg_plan(L.n, L.n, B, true, n_steps, passes, 4);
+  const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes, 4);
+  // The result goes out by TMA where its rows are whole 16-byte pieces.
+  const bool direct = !tall && L.k % 8 != 0;
   for (int i = 0; i < steps; ++i) {
     const double* c = coefficients + 3 * i;
     const int from = i & 1, to = from ^ 1;
@@ -572,7 +675,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     TgProblem g;
     g.bf16 = false;
     g.batch = B;
-    g.passes = L.split ? 3 : 1;
+    g.passes = passes;
     // A = X X^T
     g.M = g.N = L.n;
     g.Kc = L.k;
@@ -582,9 +685,16 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.a.ld = L.ldx;
     g.a.batch_stride = xb;
     g.b = g.a;
+    g.out.p = half_at(L.R);
+    g.out.lo = R_lo;
+    g.out.ld = L.ldr;
+    g.out.batch_stride = rb;
+    g.out.batch = B;
+    g.out.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    g.plan = gram_plan;
     OrthoGram::Params gram{D, half_at(L.R), R_lo, L.ldr, rb, static_cast<float>(1.0 / (sx * sx)),
                            static_cast<float>(sr / (sx * sx))};
-    st = launch_tg<OrthoGram>(*ds, g, sym_pairs, gram, s);
+    st = launch_tg_split<OrthoGram>(*ds, g, gram, s);
     if (st != BITNET_OK) return st;
     // R R -> Q, E
     g.Kc = L.n;
@@ -593,11 +703,15 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.a.ld = L.ldr;
     g.a.batch_stride = rb;
     g.b = g.a;
-    OrthoPoly::Params poly_p{D, E, half_at(L.R), R_lo, half_at(L.Q), Q_lo, L.ldr, rb,
-                             static_cast<float>(c[0]), static_cast<float>(c[1]),
-                             static_cast<float>(c[2]), static_cast<float>(1.0 / (sr * sr)),
-                             static_cast<float>(1.0 / sr), static_cast<float>(sq)};
-    st = launch_tg<OrthoPoly>(*ds, g, sym_pairs, poly_p, s);
+    g.in = g.out;
+    g.out.p = half_at(L.Q);
+    g.out.lo = Q_lo;
+    g.plan = poly_plan;
+    OrthoPoly::Params poly_p{D, E, half_at(L.Q), Q_lo, L.ldr, rb, static_cast<float>(c[0]),
+                             static_cast<float>(c[1]), static_cast<float>(c[2]),
+                             static_cast<float>(1.0 / (sr * sr)), static_cast<float>(1.0 / sr),
+                             static_cast<float>(sq)};
+    st = launch_tg_split<OrthoPoly>(*ds, g, poly_p, s);
     if (st != BITNET_OK) return st;
     // X <- E X + Q X
     g.sym = false;
@@ -609,13 +723,28 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.b.ld = L.ldx;
     g.b.batch_stride = xb;
     g.b.mn = true;
+    g.in.p = g.b.p;
+    g.in.lo = g.b.lo;
+    g.in.ld = L.ldx;
+    g.in.batch_stride = xb;
     const bool last = i == steps - 1;
-    OrthoUpdate::Params up{E, half_at(L.X[from]), half_at(L.X_lo[from]),
-                           last ? nullptr : half_at(L.X[to]), half_at(L.X_lo[to]), L.ldx, xb,
-                           static_cast<__nv_bfloat16*>(O), tall ? 1 : 0,
-                           static_cast<float>(1.0 / (sq * sx)), static_cast<float>(1.0 / sx),
-                           static_cast<float>(sy)};
-    st = launch_tg<OrthoUpdate>(*ds, g, x_pairs, up, s);
+    g.out = g.in;
+    g.out.p = half_at(L.X[to]);
+    g.out.lo = half_at(L.X_lo[to]);
+    if (last) {
+      g.out = TgTensor{};
+      if (!tall && !direct) {
+        g.out.p = O;
+        g.out.ld = L.k;
+        g.out.batch_stride = L.n * L.k;
+        g.out.batch = B;
+      }
+    }
+    g.plan = update_plan;
+    OrthoUpdate::Params up{E, last ? static_cast<__nv_bfloat16*>(O) : nullptr, tall ? 1 : 0,
+                           direct ? 1 : 0, static_cast<float>(1.0 / (sq * sx)),
+                           static_cast<float>(1.0 / sx), static_cast<float>(sy)};
+    st = launch_tg_split<OrthoUpdate>(*ds, g, up, s);
     if (st != BITNET_OK) return st;
     sx = sy;
   }
