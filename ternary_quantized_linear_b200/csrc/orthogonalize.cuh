@@ -73,53 +73,108 @@ ortho_norm_kernel(const void* __restrict__ U, int u_bf16, int64_t size,
   if (threadIdx.x == 0) part[blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x] = red[0];
 }
 
-// X = U / (||U||_F + eps) times `scale`, as two halves, [n][ldx], from U
-// [rows][cols] (transposed when `tall`), one 32 x 32 tile per block.
+// 1 / (||U||_F + eps) of matrix b from the blocks' sums, in a fixed order;
+// all 256 threads of a block.
+__device__ __forceinline__ double ortho_inverse_norm(const double* part, int parts, int b,
+                                                     float eps, double* red) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < parts; i += 256)
+    s += __ldcg(part + static_cast<int64_t>(b) * parts + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+  const double norm = sqrt(s) + static_cast<double>(eps);
+  return norm > 0.0 ? 1.0 / norm : 0.0;  // eps = 0 and U = 0: X = 0
+}
+
+// X = U / (||U||_F + eps) times `scale`, as two halves, [n][ldx], from a wide
+// U [n][k]: eight elements per thread and round (U's rows 16-byte aligned when
+// `vec`; the last columns of a row may be padding of X).
 __global__ void __launch_bounds__(256)
-ortho_start_kernel(const void* __restrict__ U, int u_bf16, int rows, int cols, int tall,
+ortho_start_kernel(const void* __restrict__ U, int u_bf16, int64_t n, int64_t k, int vec,
                    const double* __restrict__ part, int parts, float eps, float scale,
-                   uint16_t* __restrict__ hi, uint16_t* __restrict__ lo, int64_t ldx,
-                   int64_t x_batch) {
-  __shared__ double red[256];
-  __shared__ float tile[32][33];
+                   uint16_t* __restrict__ hi, uint16_t* __restrict__ lo, int64_t ldx) {
+  __shared__ double red[8];
+  const int b = blockIdx.y;
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const double inv = ortho_inverse_norm(part, parts, b, eps, red);
+  const int64_t per_row = (k + 7) >> 3, total = n * per_row;
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
+    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+    const int64_t at = (static_cast<int64_t>(b) * n + r) * k + c;
+    float v[8];
+    if (vec) {
+      if (u_bf16) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(U) + at));
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = bf16_bits_to_f32(ws[j] & 0xFFFFu);
+          v[2 * j + 1] = bf16_bits_to_f32(ws[j] >> 16);
+        }
+      } else {
+        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(U) + at);
+        const float4 x = __ldg(s), y = __ldg(s + 1);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < k ? ortho_load(U, u_bf16 != 0, at + j) : 0.0f;
+    }
+    __align__(16) uint16_t h[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      split_half(static_cast<float>(v[j] * inv) * scale, h[j], l[j]);
+    const int64_t o = (static_cast<int64_t>(b) * n + r) * ldx + c;
+    *reinterpret_cast<uint4*>(hi + o) = *reinterpret_cast<const uint4*>(h);
+    *reinterpret_cast<uint4*>(lo + o) = *reinterpret_cast<const uint4*>(l);
+  }
+}
+
+// The same, transposed, from a tall U [rows][cols]: 64 x 32 tiles through
+// shared memory (64 rows of U become 64 neighbouring entries of X's rows).
+__global__ void __launch_bounds__(256)
+ortho_start_tall_kernel(const void* __restrict__ U, int u_bf16, int rows, int cols,
+                        const double* __restrict__ part, int parts, float eps, float scale,
+                        uint16_t* __restrict__ hi, uint16_t* __restrict__ lo, int64_t ldx) {
+  __shared__ double red[8];
+  __shared__ float tile[32][65];
   const int b = blockIdx.z;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 256) s += part[static_cast<int64_t>(b) * parts + i];
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int h = 128; h > 0; h >>= 1) {
-    if (threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
-    __syncthreads();
-  }
-  const double norm = sqrt(red[0]) + static_cast<double>(eps);
-  const double inv = norm > 0.0 ? 1.0 / norm : 0.0;  // eps = 0 and U = 0: X = 0
+  const double inv = ortho_inverse_norm(part, parts, b, eps, red);
   const int64_t base = static_cast<int64_t>(b) * rows * cols;
-  const int r0 = blockIdx.y * 32, c0 = blockIdx.x * 32;
+  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 32;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  for (int i = ty; i < 32; i += 8) {
+#pragma unroll
+  for (int i = ty; i < 64; i += 8) {
     const int r = r0 + i, c = c0 + tx;
-    float v = 0.0f;
-    if (r < rows && c < cols)
-      v = static_cast<float>(ortho_load(U, u_bf16 != 0, base + static_cast<int64_t>(r) * cols + c) *
-                             inv) *
-          scale;
-    tile[i][tx] = v;
+    tile[tx][i] = r < rows && c < cols
+                      ? ortho_load(U, u_bf16 != 0, base + static_cast<int64_t>(r) * cols + c)
+                      : 0.0f;
   }
   __syncthreads();
+#pragma unroll
   for (int i = ty; i < 32; i += 8) {
-    const int r = tall ? c0 + i : r0 + i, c = tall ? r0 + tx : c0 + tx;
-    if (r < (tall ? cols : rows) && c < (tall ? rows : cols)) {
-      const int64_t o = b * x_batch + static_cast<int64_t>(r) * ldx + c;
-      split_half(tall ? tile[tx][i] : tile[i][tx], hi[o], lo[o]);
+    const int c = c0 + i, r = r0 + 2 * tx;
+    if (c < cols && r < rows) {  // rows past the last one are padding of X
+      uint16_t h[2], l[2];
+      split_half(static_cast<float>(tile[i][2 * tx] * inv) * scale, h[0], l[0]);
+      split_half(static_cast<float>(tile[i][2 * tx + 1] * inv) * scale, h[1], l[1]);
+      const int64_t o = (static_cast<int64_t>(b) * cols + c) * ldx + r;
+      *reinterpret_cast<uint32_t*>(hi + o) = h[0] | (static_cast<uint32_t>(h[1]) << 16);
+      *reinterpret_cast<uint32_t*>(lo + o) = l[0] | (static_cast<uint32_t>(l[1]) << 16);
     }
   }
 }
 
-// Of a tile below the diagonal of a symmetric product, the mirrored entries:
-// lanes hold neighbouring rows, so a store of one column is 64 contiguous
-// bytes.
+// Transposed entries straight to memory: lanes hold neighbouring rows, so a
+// store of one column is 64 contiguous bytes.
 __device__ __forceinline__ void ortho_store_mirror(uint16_t* base, int64_t ld, int row, int col,
                                                    const uint32_t (&w)[16], int n) {
 #pragma unroll
@@ -152,27 +207,37 @@ __device__ __forceinline__ void ortho_pack_rest(const float (&v)[32], const uint
   }
 }
 
-// A block (and the low halves behind it) out by TMA, mirrored when asked.
+// A block out by TMA, with the low halves behind it (low), or with its mirror
+// image behind it (mirror, a tile below the diagonal of a symmetric product):
+// element (r, j) of the chunk goes to piece r / 8 of row j there.
 __device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const TgPart& t,
                                             uint8_t* blk, int col, const float (&v)[32],
-                                            bool low, bool mirror, uint16_t* base,
-                                            uint16_t* base_lo, int64_t ld, int N) {
-  uint32_t w[16], lo[16];
+                                            bool low, bool mirror, int rows) {
+  uint32_t w[16];
   ortho_pack(v, w);
   block16_write(blk, st.lane, w);
   if (low) {
+    uint32_t lo[16];
     ortho_pack_rest(v, w, lo);
     block16_write(blk + 2048, st.lane, lo);
+  } else if (mirror) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      *reinterpret_cast<uint16_t*>(blk + 2048 + j * 64 +
+                                   (((st.lane >> 3) ^ ((j >> 1) & 3)) << 4) +
+                                   (st.lane & 7) * 2) =
+          static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
   }
   fence_proxy_async_smem();
   __syncwarp();
-  tg_store_block(st, &m.out, blk, col, t);
-  if (low) tg_store_block(st, &m.out_lo, blk + 2048, col, t);
-  if (st.lane == 0) bulk_commit();
-  if (mirror && t.live) {
-    ortho_store_mirror(base, ld, t.row, col, w, min(32, N - col));
-    if (low) ortho_store_mirror(base_lo, ld, t.row, col, lo, min(32, N - col));
+  if (st.lane == 0 && !t.dry) {
+    tma_store_3d(&m.out, smem_u32(blk), col, t.row0, t.tile.b);
+    if (low)
+      tma_store_3d(&m.out_lo, smem_u32(blk + 2048), col, t.row0, t.tile.b);
+    else if (mirror && t.row0 < rows)
+      tma_store_3d(&m.out, smem_u32(blk + 2048), t.row0, col, t.tile.b);
   }
+  if (st.lane == 0) bulk_commit();
 }
 
 // A = X X^T: its diagonal to D (fp32), the rest to R (fp16, and its low half
@@ -181,8 +246,7 @@ struct OrthoGram {
   static constexpr int kSlots = 2, kSlotBytes = 4096;
   struct Params {
     float* D;              // [batch][n]
-    uint16_t *R, *R_lo;    // [batch][n][ld]; R_lo may be null
-    int64_t ld, batch;     // row stride, batch stride (elements)
+    int low;               // R's low half too (then not symmetric tiles)
     float to_true, to_R;   // accumulator -> A, accumulator -> stored R
   };
   static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
@@ -191,8 +255,7 @@ struct OrthoGram {
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
                                              const TgPart& t, TgStage& st, Src src) {
-    const bool mirror = t.tile.m != t.tile.n;
-    const int64_t base = t.tile.b * e.batch;
+    const bool mirror = p.sym && t.tile.m != t.tile.n;
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
@@ -209,8 +272,7 @@ struct OrthoGram {
       }
       if (t.live && at >= 0 && at < 32)
         e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.to_true;
-      ortho_store(st, m, t, tg_out_block<OrthoGram>(st), col, v, e.R_lo != nullptr, mirror,
-                  e.R + base, e.R_lo + base, e.ld, p.N);
+      ortho_store(st, m, t, tg_out_block<OrthoGram>(st), col, v, e.low != 0, mirror, p.M);
     }
   }
 };
@@ -221,15 +283,14 @@ struct OrthoPoly {
   struct Params {
     const float* D;
     float* E;              // [batch][n]: a + b D + c (D^2 + (R R)_ii)
-    uint16_t *Q, *Q_lo;    // Q_lo may be null (then R has no low half either)
-    int64_t ld, batch;
+    int low;               // R and Q with their low halves (then not symmetric tiles)
     float a, b, c;
     float acc_true, r_true, to_Q;
   };
   using In = TgInput<OrthoPoly>;
   static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
                                                const TgPart& t) {
-    In::begin(st, m, t, e.Q_lo != nullptr, 2048);
+    In::begin(st, m, t, e.low != 0, 2048);
   }
   static __device__ __forceinline__ void abandon(TgStage& st, const Params&, const TgPart& t) {
     In::abandon(st, t);
@@ -237,10 +298,9 @@ struct OrthoPoly {
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
                                              const TgPart& t, TgStage& st, Src src) {
-    const bool mirror = t.tile.m != t.tile.n, low = e.Q_lo != nullptr;
+    const bool mirror = p.sym && t.tile.m != t.tile.n, low = e.low != 0;
     const float* D = e.D + static_cast<int64_t>(t.tile.b) * p.M;
     const float di = t.live ? __ldcg(D + t.row) : 0.0f;
-    const int64_t base = t.tile.b * e.batch;
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
@@ -282,7 +342,7 @@ struct OrthoPoly {
         e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
             e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr_ii), e.b * di);
       __syncwarp();  // the whole block was read
-      ortho_store(st, m, t, blk, col, v, low, mirror, e.Q + base, e.Q_lo + base, e.ld, p.N);
+      ortho_store(st, m, t, blk, col, v, low, mirror, p.M);
       In::next(st, m, t, k, low, 2048);
     }
   }
@@ -342,7 +402,7 @@ struct OrthoUpdate {
       if (!e.out) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= e.to_Y;
-        ortho_store(st, m, t, blk, col, v, true, false, nullptr, nullptr, 0, p.N);
+        ortho_store(st, m, t, blk, col, v, true, false, p.M);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);

@@ -62,8 +62,8 @@ struct TgCfg {
   static constexpr uint32_t TMEM_COLS = 2 * BN;  // two accumulators
   static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
-  // full, empty, accfull[2], accempty[2], drain, one per epilogue block
-  static constexpr int NBAR = 2 * STAGES + 5 + kTgEpiWarps * Epi::kSlots;
+  // full, empty, accfull[2], accempty[2], drain, parts, one per epilogue block
+  static constexpr int NBAR = 2 * STAGES + 6 + kTgEpiWarps * Epi::kSlots;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_DYN = OFF_MISC + 16 + 1024;
   static_assert(BN == 128 || BN == 256, "BN");
@@ -433,23 +433,33 @@ struct TgTmemSrc {
   }
 };
 
+// Parts of a cluster's CTAs, [SPLIT][columns of this CTA][128 rows] fp32 in
+// this CTA's shared memory, added in rank order.
 template <int SPLIT>
 struct TgClusterSrc {
-  uint32_t addr[SPLIT];  // of this thread's row in each CTA's [column][128] fp32 part
+  const float* parts;  // of this thread's row
+  int first;           // the CTA's first column of the tile
   __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
+    const float* at = parts + (c - first) * 128;
 #pragma unroll
-    for (int s = 0; s < SPLIT; ++s) {
+    for (int i = 0; i < 32; ++i) {
+      float v = at[i * 128];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float v;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(v)
-                     : "r"(addr[s] + static_cast<uint32_t>((c + i) * 512)));
-        r[i] = s == 0 ? __float_as_uint(v) : __float_as_uint(__fadd_rn(__uint_as_float(r[i]), v));
-      }
+      for (int s = 1; s < SPLIT; ++s) v = __fadd_rn(v, at[s * (128 / SPLIT) * 128 + i * 128]);
+      r[i] = __float_as_uint(v);
     }
   }
 };
+
+// Copy shared memory to another CTA of the cluster, counted on its barrier.
+__device__ __forceinline__ void dsmem_copy(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
+                                           uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(dst_cluster),
+      "r"(src), "r"(bytes), "r"(bar_cluster)
+      : "memory");
+}
 
 // ------------------------------------------------------------------- kernel
 
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
 tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
                const typename Epi::Params ep) {
   using C = TgCfg<CG, BN, Epi>;
-  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::OFF_EPI >= 65536), "split");
+  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::OFF_EPI >= 131072), "split");
   extern __shared__ uint8_t tg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(tg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -470,7 +480,8 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   uint64_t* accfull = empty + C::STAGES;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
-  uint64_t* epi_bars = drain + 1;
+  uint64_t* parts_bar = drain + 1;
+  uint64_t* epi_bars = parts_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -493,6 +504,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       mbar_init(&accempty[i], CG * kTgEpiWarps);
     }
     mbar_init(drain, 1);
+    mbar_init(parts_bar, 1);
     for (int i = 0; i < kTgEpiWarps * Epi::kSlots; ++i) mbar_init(&epi_bars[i], 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -649,10 +661,8 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       if constexpr (SPLIT == 1) {
         Epi::run(ep, p, maps, t, st, TgTmemSrc{lanes});
       } else {
-        TgClusterSrc<SPLIT> src;
-#pragma unroll
-        for (int s = 0; s < SPLIT; ++s) src.addr[s] = map_to_rank(smem_u32(smem), rank);
-        Epi::run(ep, p, maps, t, st, src);
+        Epi::run(ep, p, maps, t, st,
+                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem), 0});
       }
       st.seq = 0;
     }
@@ -699,21 +709,38 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   }
   __syncwarp();
   if constexpr (SPLIT > 1) {
-    // One tile per cluster: its parts meet, and CTA r finishes columns
-    // [128 r / SPLIT, 128 (r + 1) / SPLIT), a chunk of 32 per warp.
-    __syncthreads();
-    cluster_sync();
+    // One tile per cluster: CTA r finishes columns [128 r / SPLIT, 128 (r + 1)
+    // / SPLIT), a chunk of 32 per warp.  The ring's first half holds this
+    // CTA's part, its second half receives the CTA's columns of every part.
     constexpr int kChunks = 4 / SPLIT;
-    if (warp >= 4 && half < kChunks && *abort_flag == 0) {
-      TgPart part = part_of(tg_tile(p, worker), q, half);
-      part.first = 32 * (static_cast<int>(rank) * kChunks + half);
-      part.step = 1 << 20;
-      TgClusterSrc<SPLIT> src;
+    constexpr uint32_t kShare = 65536 / SPLIT;
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(parts_bar, 65536);
+    cluster_sync();
+    if (threadIdx.x == 0) {
+      const uint32_t base = smem_u32(smem);
 #pragma unroll
       for (int s = 0; s < SPLIT; ++s)
-        src.addr[s] = map_to_rank(smem_u32(smem), s) + static_cast<uint32_t>(4 * (32 * q + lane));
-      Epi::begin(st, maps, ep, part);
-      Epi::run(ep, p, maps, part, st, src);
+        dsmem_copy(map_to_rank(base + 65536u + rank * kShare, s), base + s * kShare, kShare,
+                   map_to_rank(smem_u32(parts_bar), s));
+    }
+    const TgPart whole = part_of(tg_tile(p, worker), q, half);
+    if (warp >= 4 && half < kChunks) {
+      TgPart part = whole;
+      part.first = 32 * (static_cast<int>(rank) * kChunks + half);
+      part.step = 1 << 20;
+      const bool run = *abort_flag == 0;
+      if (run) Epi::begin(st, maps, ep, part);
+      const bool ok = __all_sync(0xFFFFFFFFu,
+                                 mbar_wait_bounded(parts_bar, 0u, nullptr, limit));
+      if (!ok && lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
+      if (run && ok)
+        Epi::run(ep, p, maps, part, st,
+                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem) + 16384 + 32 * q + lane,
+                                     static_cast<int>(rank) * 32 * kChunks});
+      else if (run)
+        Epi::abandon(st, ep, part);
     }
     __syncwarp();
   }

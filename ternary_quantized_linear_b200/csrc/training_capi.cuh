@@ -101,13 +101,16 @@ int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) 
 // its epilogue.  A pair's 64-k step takes 660 cycles (measured; the MMAs
 // alone 512), a 128 x 128 step 600 (32 KiB at 64 bytes a cycle are 512; the
 // MMAs 256); the epilogue and what a launch waits for come on top of each
-// wave, and for a cluster's split the meeting of the parts.
+// wave, and for a cluster's split the meeting of the parts.  Of clusters of
+// two SMs 74 are resident at a time, of four 33 (the occupancy query's answer
+// on a B200: its SM groups do not divide into fours).
 double tg_cost(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, const TgPlan& pl) {
   const int64_t tiles = tg_tiles(M, N, batch, sym, 128 * pl.cg, pl.bn);
-  const double waves = static_cast<double>(ceil_div(tiles * pl.split, kPlanSms / pl.cg));
+  const int64_t slots = pl.split == 4 ? 33 : kPlanSms / std::max(pl.cg, pl.split);
+  const double waves = static_cast<double>(ceil_div(tiles, slots));
   if (pl.cg == 2) return waves * (660.0 * static_cast<double>(steps) + 5000.0);
   return waves * (600.0 * static_cast<double>(ceil_div(steps, pl.split)) + 3000.0 +
-                  (pl.split > 1 ? 2500.0 : 0.0));
+                  (pl.split > 1 ? 1500.0 : 0.0));
 }
 
 // Pairs on 256 x 256 tiles, or single SMs on 128 x 128 tiles, each tile's
@@ -652,18 +655,26 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
                   kOrthoNormThreads, s, U, u_bf16, N * K, norm);
   if (st != BITNET_OK) return st;
   double sx = fp16_scale(top[0]);
-  st = launch_pdl(ortho_start_kernel,
-                  dim3(static_cast<unsigned>(ceil_div(K, 32)),
-                       static_cast<unsigned>(ceil_div(N, 32)), static_cast<unsigned>(B)),
-                  256, s, U, u_bf16, static_cast<int>(N), static_cast<int>(K), tall ? 1 : 0, norm,
-                  L.parts, eps, static_cast<float>(sx), half_at(L.X[0]), half_at(L.X_lo[0]),
-                  L.ldx, xb);
+  if (tall) {
+    st = launch_pdl(ortho_start_tall_kernel,
+                    dim3(static_cast<unsigned>(ceil_div(N, 64)),
+                         static_cast<unsigned>(ceil_div(K, 32)), static_cast<unsigned>(B)),
+                    256, s, U, u_bf16, static_cast<int>(N), static_cast<int>(K), norm, L.parts,
+                    eps, static_cast<float>(sx), half_at(L.X[0]), half_at(L.X_lo[0]), L.ldx);
+  } else {
+    const int64_t work = ceil_div(N * ceil_div(K, 8), 256);
+    const int64_t blocks = std::min<int64_t>(work, std::max<int64_t>(1, 16LL * ds->num_sms / B));
+    st = launch_pdl(ortho_start_kernel,
+                    dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(B)), 256, s, U,
+                    u_bf16, N, K, K % 8 == 0 ? 1 : 0, norm, L.parts, eps, static_cast<float>(sx),
+                    half_at(L.X[0]), half_at(L.X_lo[0]), L.ldx);
+  }
   if (st != BITNET_OK) return st;
 
   const int passes = L.split ? 3 : 1;
   const int64_t n_steps = ceil_div(L.n, kTgKStep), k_steps = ceil_div(L.k, kTgKStep);
-  const TgPlan gram_plan = tg_plan(L.n, L.n, B, true, k_steps, passes, 4);
-  const TgPlan poly_plan = tg_plan(L.n, L.n, B, true, n_steps, passes, 4);
+  const TgPlan gram_plan = tg_plan(L.n, L.n, B, !L.split, k_steps, passes, 4);
+  const TgPlan poly_plan = tg_plan(L.n, L.n, B, !L.split, n_steps, passes, 4);
   const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes, 4);
   // The result goes out by TMA where its rows are whole 16-byte pieces.
   const bool direct = !tall && L.k % 8 != 0;
@@ -679,7 +690,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     // A = X X^T
     g.M = g.N = L.n;
     g.Kc = L.k;
-    g.sym = true;
+    g.sym = !L.split;
     g.a.p = half_at(L.X[from]);
     g.a.lo = half_at(L.X_lo[from]);
     g.a.ld = L.ldx;
@@ -692,7 +703,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.out.batch = B;
     g.out.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     g.plan = gram_plan;
-    OrthoGram::Params gram{D, half_at(L.R), R_lo, L.ldr, rb, static_cast<float>(1.0 / (sx * sx)),
+    OrthoGram::Params gram{D, L.split ? 1 : 0, static_cast<float>(1.0 / (sx * sx)),
                            static_cast<float>(sr / (sx * sx))};
     st = launch_tg_split<OrthoGram>(*ds, g, gram, s);
     if (st != BITNET_OK) return st;
@@ -707,7 +718,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.out.p = half_at(L.Q);
     g.out.lo = Q_lo;
     g.plan = poly_plan;
-    OrthoPoly::Params poly_p{D, E, half_at(L.Q), Q_lo, L.ldr, rb, static_cast<float>(c[0]),
+    OrthoPoly::Params poly_p{D, E, L.split ? 1 : 0, static_cast<float>(c[0]),
                              static_cast<float>(c[1]), static_cast<float>(c[2]),
                              static_cast<float>(1.0 / (sr * sr)), static_cast<float>(1.0 / sr),
                              static_cast<float>(sq)};
