@@ -432,4 +432,375 @@ struct OrthoUpdate {
   }
 };
 
+// ------------------------------------------------- small updates in one launch
+
+// n <= 128 and k <= 2048: all steps in one launch, X, R and Q in shared
+// memory.  Sixteen launches of a few microseconds of latency each were 150 us
+// for a 128 x 128 update whose products take 5.
+//
+// A cluster of `cluster` CTAs holds one matrix, each CTA `ks` columns of X
+// (K-major for A = X X^T; the same bytes are the MN-major operand of Q X).
+// Per step: each CTA's part of A goes to the CTAs that own its columns, which
+// add the parts in rank order and hand R and D to all; every CTA forms Q for
+// itself (128^3 is cheaper than an exchange) and updates its own columns.
+// The products take both halves of their operands (three MMAs for one).
+// Threads: 16 warps; warp w has TMEM lanes 32 (w % 4) .. +31, a row each, and
+// the columns of group w / 4.  Thread 0 issues the MMAs.
+
+constexpr int kOsThreads = 512;
+constexpr int kOsMaxKs = 256;
+
+struct OsStep {
+  float a, b, c;
+  float gram_true, gram_R;       // accumulator -> A, accumulator -> stored R
+  float poly_true, r_true, to_Q;
+  float upd_true, x_true, to_Y;
+};
+
+struct OsParams {
+  const void* U;
+  __nv_bfloat16* out;
+  int u_bf16, n, k, tall, cluster, ks, steps;
+  float eps, scale;              // of the first X
+  int* status;
+  uint64_t wait_limit_ns;
+  OsStep step[32];
+};
+
+struct OsSmem {
+  static constexpr int OFF_X = 0;                         // hi: ks / 64 blocks of 128 x 64
+  static constexpr int OFF_X_LO = kOsMaxKs / 64 * 16384;
+  static constexpr int OFF_R = 2 * OFF_X_LO;              // hi: 2 blocks; the parts before it
+  static constexpr int OFF_R_LO = OFF_R + 32768;
+  static constexpr int OFF_D = OFF_R + 65536;
+  static constexpr int OFF_E = OFF_D + 512;
+  static constexpr int OFF_RED = OFF_E + 512;             // 16 + 8 doubles
+  static constexpr int OFF_BAR = OFF_RED + 192;
+  static constexpr int SMEM_DYN = OFF_BAR + 32 + 1024;
+  static_assert(SMEM_DYN <= 232448, "shared memory");
+};
+
+// Byte of element (row, col) in 128-byte swizzled blocks of 128 rows x 64.
+__device__ __forceinline__ int os_at(int row, int col) {
+  return (col >> 6) * 16384 + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+// MN-major descriptor of such blocks (64 columns of the block are the MN
+// extent, its 128 rows the contraction): the next 64 columns 16384 bytes on.
+__device__ __forceinline__ uint64_t os_desc_mn(uint32_t smem_addr) {
+  uint64_t d = umma_desc_sw128_mnmajor(smem_addr);
+  d &= ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return d | (static_cast<uint64_t>(16384u >> 4) << 16);
+}
+
+__device__ __forceinline__ void os_read16(const uint8_t* hi, const uint8_t* lo, int row, int col,
+                                          float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint4 h = *reinterpret_cast<const uint4*>(hi + os_at(row, col + 8 * j));
+    const uint4 l = *reinterpret_cast<const uint4*>(lo + os_at(row, col + 8 * j));
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = half2_bits_to_f32(hw[i]), b = half2_bits_to_f32(lw[i]);
+      v[8 * j + 2 * i] = a.x + b.x;
+      v[8 * j + 2 * i + 1] = a.y + b.y;
+    }
+  }
+}
+
+__device__ __forceinline__ void os_write16(uint8_t* hi, uint8_t* lo, int row, int col,
+                                           const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[8 * j + 2 * i], y = v[8 * j + 2 * i + 1];
+      const __half2 p = __floats2half2_rn(x, y);
+      h[i] = *reinterpret_cast<const uint32_t*>(&p);
+      const float2 f = __half22float2(p);
+      const __half2 q = __floats2half2_rn(x - f.x, y - f.y);
+      l[i] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    *reinterpret_cast<uint4*>(hi + os_at(row, col + 8 * j)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(lo + os_at(row, col + 8 * j)) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+// All writes to shared memory (of this or another CTA) before, all operand
+// reads after.
+__device__ __forceinline__ void os_sync(bool cluster) {
+  asm volatile("fence.proxy.async;" ::: "memory");
+  tc_fence_before_sync();
+  if (cluster)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+}
+
+__global__ void __launch_bounds__(kOsThreads, 1)
+ortho_small_kernel(const __grid_constant__ OsParams p) {
+  using L = OsSmem;
+  extern __shared__ uint8_t os_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(os_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *Xh = smem + L::OFF_X, *Xl = smem + L::OFF_X_LO;
+  uint8_t *Rh = smem + L::OFF_R, *Rl = smem + L::OFF_R_LO;
+  float* D = reinterpret_cast<float*>(smem + L::OFF_D);
+  float* E = reinterpret_cast<float*>(smem + L::OFF_E);
+  double* red = reinterpret_cast<double*>(smem + L::OFF_RED);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 16);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, grp = warp >> 2;
+  const int row = 32 * q + lane;
+  const bool many = p.cluster > 1;
+  const uint32_t rank = many ? cluster_rank() : 0u;
+  const int64_t b = blockIdx.x / p.cluster;
+  const int c0 = static_cast<int>(rank) * p.ks;
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (many) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+
+  // ||U||_F: fp64 squares, a fixed order inside the CTA, then rank order.
+  const int64_t base = b * p.n * p.k;
+  const int width = max(0, min(p.ks, p.k - c0));  // this CTA's columns of X
+  auto u_at = [&](int r, int c) {                  // X's element (r, c0 + c) in U
+    return p.tall ? base + static_cast<int64_t>(c0 + c) * p.n + r
+                  : base + static_cast<int64_t>(r) * p.k + c0 + c;
+  };
+  const int fast = p.tall ? p.n : width;           // neighbours in memory
+  const int count = p.n * width;
+  double s = 0.0;
+  for (int i = tid; i < count; i += kOsThreads) {
+    const int slow = i / fast, f = i - slow * fast;
+    const double v = ortho_load(p.U, p.u_bf16 != 0, p.tall ? u_at(f, slow) : u_at(slow, f));
+    s += v * v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) red[warp] = s;
+  // X starts as zeros: rows past n and columns past k stay so.
+  for (int i = tid; i < p.ks / 64 * 1024; i += kOsThreads) {
+    reinterpret_cast<uint4*>(Xh)[i] = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4*>(Xl)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    s = 0.0;
+    for (int i = 0; i < kOsThreads / 32; ++i) s += red[i];
+    if (!many) {
+      red[16] = s;
+    } else {
+      for (int i = 0; i < p.cluster; ++i)
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
+                         map_to_rank(smem_u32(red + 16 + rank), i)),
+                     "d"(s)
+                     : "memory");
+    }
+  }
+  os_sync(many);
+  s = 0.0;
+  for (int i = 0; i < p.cluster; ++i) s += red[16 + i];
+  const double norm = sqrt(s) + static_cast<double>(p.eps);
+  const double inv = norm > 0.0 ? 1.0 / norm : 0.0;  // eps = 0 and U = 0: X = 0
+  for (int i = tid; i < count; i += kOsThreads) {
+    const int slow = i / fast, f = i - slow * fast;
+    const int r = p.tall ? f : slow, c = p.tall ? slow : f;
+    uint16_t h, l;
+    split_half(static_cast<float>(ortho_load(p.U, p.u_bf16 != 0, u_at(r, c)) * inv) * p.scale, h,
+               l);
+    *reinterpret_cast<uint16_t*>(Xh + os_at(r, c)) = h;
+    *reinterpret_cast<uint16_t*>(Xl + os_at(r, c)) = l;
+  }
+  os_sync(false);
+
+  uint32_t phase = 0;
+  auto wait_mma = [&]() {
+    if (*abort_flag == 0 && !mbar_wait_bounded(bar, phase, abort_flag, p.wait_limit_ns)) {
+      *abort_flag = 1;
+      record_failure(p.status, DEV_TIMEOUT_MMA);
+    }
+    phase ^= 1u;
+    __syncwarp();
+    tc_fence_after_sync();
+  };
+  // D[tmem + col] = sum over the contraction of A B^T, hi hi + hi lo + lo hi;
+  // A K-major at a_hi / a_lo, B K-major or MN-major.
+  auto issue = [&](uint32_t col, const uint8_t* a_hi, const uint8_t* a_lo, const uint8_t* b_hi,
+                   const uint8_t* b_lo, int k16, bool b_mn, uint32_t idesc) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const uint32_t a = smem_u32(pass == 2 ? a_lo : a_hi), bb = smem_u32(pass == 1 ? b_lo : b_hi);
+      for (int i = 0; i < k16; ++i) {
+        const uint32_t off = (i >> 2) * 16384 + (i & 3) * 32;  // K-major: 16 columns on
+        tg_mma<1>(tmem + col, umma_desc_sw128_kmajor(a + off),
+                  b_mn ? os_desc_mn(bb + i * 2048) : umma_desc_sw128_kmajor(bb + off), idesc,
+                  (pass > 0 || i > 0) ? 1u : 0u);
+      }
+    }
+    tc_commit(bar);
+  };
+  constexpr uint32_t kGramCol = 0, kPolyCol = 128, kUpdCol = 256;
+  const uint32_t sq_desc = tg_idesc(128, 128, false, false, false);
+  const uint32_t upd_desc = tg_idesc(128, p.ks, false, false, true);
+
+  for (int it = 0; it < p.steps; ++it) {
+    const OsStep& c = p.step[it];
+    // A = X X^T, this CTA's columns of X
+    if (tid == 0) issue(kGramCol, Xh, Xl, Xh, Xl, p.ks / 16, false, sq_desc);
+    wait_mma();
+    if (!many) {
+#pragma unroll 1
+      for (int j = 32 * grp; j < 32 * grp + 32; j += 16) {
+        uint32_t r[16];
+        float v[16];
+        tmem_ld_32x32b_x16(lanes + kGramCol + j, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float z = __uint_as_float(r[i]);
+          if (j + i == row) D[row] = z * c.gram_true;
+          v[i] = j + i == row ? 0.0f : z * c.gram_R;
+        }
+        os_write16(Rh, Rl, row, j, v);
+      }
+      os_sync(false);
+    } else {
+      // Part `rank` of columns [share * o, +share) to CTA o: [rank][column][row].
+      const int share = 128 / p.cluster;
+#pragma unroll 1
+      for (int j = 32 * grp; j < 32 * grp + 32; j += 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(lanes + kGramCol + j, r);
+        tmem_ld_wait();
+        const uint32_t owner = static_cast<uint32_t>(j / share);  // 16 columns, one owner
+        const uint32_t at = map_to_rank(
+            smem_u32(Rh) + static_cast<uint32_t>(
+                               ((static_cast<int>(rank) * share + j % share) * 128 + row) * 4),
+            owner);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + i * 512), "r"(r[i])
+                       : "memory");
+      }
+      os_sync(true);
+      // The sums of this CTA's columns, in rank order; thread (row, grp) has
+      // share / 4 of them.
+      const int mine = share / 4, first = grp * mine;
+      const float* parts = reinterpret_cast<const float*>(Rh);
+      float sum[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        sum[i] = 0.0f;
+        if (i < mine) {
+          float v = parts[(first + i) * 128 + row];
+          for (int o = 1; o < p.cluster; ++o)
+            v = __fadd_rn(v, parts[(o * share + first + i) * 128 + row]);
+          sum[i] = v;
+        }
+      }
+      os_sync(true);  // the parts were read everywhere: R may take their place
+      for (int o = 0; o < p.cluster; ++o) {
+        const uint32_t h_base = map_to_rank(smem_u32(Rh), o), l_base = map_to_rank(smem_u32(Rl), o);
+        const uint32_t d_base = map_to_rank(smem_u32(D), o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < mine) {
+            const int col = static_cast<int>(rank) * share + first + i;
+            if (col == row)
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(d_base + 4 * row),
+                           "f"(sum[i] * c.gram_true)
+                           : "memory");
+            uint16_t h, l;
+            split_half(col == row ? 0.0f : sum[i] * c.gram_R, h, l);
+            // R is symmetric: (col, row), so that lanes are neighbours
+            const uint32_t at = static_cast<uint32_t>(os_at(col, row));
+            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(h_base + at), "h"(h) : "memory");
+            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(l_base + at), "h"(l) : "memory");
+          }
+      }
+      os_sync(true);
+    }
+    // R R, and Q and a + E in its place
+    if (tid == 0) issue(kPolyCol, Rh, Rl, Rh, Rl, 8, false, sq_desc);
+    const float di = D[row];
+    wait_mma();
+#pragma unroll 1
+    for (int j = 32 * grp; j < 32 * grp + 32; j += 16) {
+      uint32_t r[16];
+      float v[16];
+      tmem_ld_32x32b_x16(lanes + kPolyCol + j, r);
+      os_read16(Rh, Rl, row, j, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float rr = __uint_as_float(r[i]) * c.poly_true;
+        const float x = v[i] * c.r_true;
+        if (j + i == row) E[row] = c.a + __fmaf_rn(c.c, __fmaf_rn(di, di, rr), c.b * di);
+        v[i] = j + i == row
+                   ? 0.0f
+                   : __fmaf_rn(c.c, __fmaf_rn(di + D[j + i], x, rr), c.b * x) * c.to_Q;
+      }
+      os_write16(Rh, Rl, row, j, v);
+    }
+    os_sync(false);
+    // X <- E X + Q X
+    if (tid == 0) issue(kUpdCol, Rh, Rl, Xh, Xl, 8, true, upd_desc);
+    const float ei = E[row] * c.x_true;
+    wait_mma();
+    const bool last = it == p.steps - 1;
+    const int quarter = p.ks / 4;
+#pragma unroll 1
+    for (int j = quarter * grp; j < quarter * grp + quarter; j += 16) {
+      uint32_t r[16];
+      float v[16];
+      tmem_ld_32x32b_x16(lanes + kUpdCol + j, r);
+      os_read16(Xh, Xl, row, j, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = __fmaf_rn(ei, v[i], __uint_as_float(r[i]) * c.upd_true);
+      if (!last) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= c.to_Y;
+        os_write16(Xh, Xl, row, j, v);
+      } else if (row < p.n) {
+        if (!p.tall && (p.k & 7) == 0 && j + 16 <= width) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+          uint4* o = reinterpret_cast<uint4*>(p.out + u_at(row, j));
+          o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (j + i < width) p.out[u_at(row, j + i)] = __float2bfloat16_rn(v[i]);
+        }
+      }
+    }
+    os_sync(many);  // Q was read everywhere: the next parts may take its place
+  }
+  if (many) cluster_sync();  // no CTA leaves while another may still reach it
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
 }  // namespace bitnet

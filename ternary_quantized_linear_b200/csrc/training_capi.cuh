@@ -347,6 +347,11 @@ constexpr int kOrthoMaxSteps = 32;
 // Largest smaller side that runs on both halves of its operands.
 constexpr int64_t kOrthoSplitN = 256;
 
+// Updates that run in one launch on clusters of up to eight CTAs.
+bool ortho_is_small(int64_t N, int64_t K) {
+  return std::min(N, K) <= 128 && std::max(N, K) <= 8 * kOsMaxKs;
+}
+
 bitnet_status check_ortho_shape(int64_t B, int64_t N, int64_t K) {
   if (B < 0 || N < 0 || K < 0) return BITNET_ERR_INVALID_ARG;
   const int64_t n = std::min(N, K), k = std::max(N, K);
@@ -429,6 +434,62 @@ double fp16_scale(double top) {
   if (!(top > 0.0)) top = 1.0;
   const int e = 14 - static_cast<int>(std::ceil(std::log2(top)));
   return std::ldexp(1.0, std::max(-40, std::min(40, e)));
+}
+
+bitnet_status launch_ortho_small(const DeviceState& ds, const void* U, int u_bf16, int64_t B,
+                                 int64_t N, int64_t K, int steps, const double* coefficients,
+                                 const double* top, const double* poly, float eps, void* O,
+                                 cudaStream_t stream) {
+  static std::once_flag once[kMaxDevices];
+  static bool ok[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BITNET_ERR_CUDA;
+  std::call_once(once[dev],
+                 [dev]() { ok[dev] = set_smem(ortho_small_kernel, OsSmem::SMEM_DYN); });
+  if (!ok[dev]) return BITNET_ERR_CUDA;
+  OsParams p{};
+  p.U = U;
+  p.out = static_cast<__nv_bfloat16*>(O);
+  p.u_bf16 = u_bf16;
+  p.n = static_cast<int>(std::min(N, K));
+  p.k = static_cast<int>(std::max(N, K));
+  p.tall = N > K ? 1 : 0;
+  p.cluster = 1;
+  while (p.cluster * kOsMaxKs < p.k) p.cluster *= 2;
+  p.ks = static_cast<int>(round_up(ceil_div(p.k, p.cluster), 64));
+  p.steps = steps;
+  p.eps = eps;
+  p.status = ds.status;
+  p.wait_limit_ns = kWaitLimitNs;
+  double sx = fp16_scale(top[0]);
+  p.scale = static_cast<float>(sx);
+  for (int i = 0; i < steps; ++i) {
+    const double* c = coefficients + 3 * i;
+    const double sr = fp16_scale(top[i] * top[i]), sq = fp16_scale(poly[i]);
+    const double sy = fp16_scale(top[i + 1]);
+    p.step[i] = OsStep{static_cast<float>(c[0]),          static_cast<float>(c[1]),
+                       static_cast<float>(c[2]),          static_cast<float>(1.0 / (sx * sx)),
+                       static_cast<float>(sr / (sx * sx)), static_cast<float>(1.0 / (sr * sr)),
+                       static_cast<float>(1.0 / sr),      static_cast<float>(sq),
+                       static_cast<float>(1.0 / (sq * sx)), static_cast<float>(1.0 / sx),
+                       static_cast<float>(sy)};
+    sx = sy;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(B * p.cluster));
+  cfg.blockDim = dim3(kOsThreads);
+  cfg.dynamicSmemBytes = OsSmem::SMEM_DYN;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cuda_status(cudaLaunchKernelEx(&cfg, ortho_small_kernel, p));
 }
 
 }  // namespace
@@ -607,7 +668,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
 }
 
 BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K) {
-  if (check_ortho_shape(B, N, K) != BITNET_OK || B == 0) return 0;
+  if (check_ortho_shape(B, N, K) != BITNET_OK || B == 0 || ortho_is_small(N, K)) return 0;
   return ortho_layout(B, N, K).total;
 }
 
@@ -633,6 +694,12 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
   if (B == 0) return BITNET_OK;
   if (!U || !O) return BITNET_ERR_INVALID_ARG;
   if (!aligned(U, 16) || !aligned(O, 16)) return BITNET_ERR_MISALIGNED;
+  if (ortho_is_small(N, K)) {
+    DeviceState* ds = device_state();
+    if (!ds) return BITNET_ERR_CUDA;
+    return launch_ortho_small(*ds, U, u_dtype == BITNET_BF16 ? 1 : 0, B, N, K, steps,
+                              coefficients, top, poly, eps, O, as_stream(stream));
+  }
   const OrthoLayout L = ortho_layout(B, N, K);
   if (!workspace || workspace_bytes < L.total) return BITNET_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BITNET_ERR_MISALIGNED;
