@@ -441,8 +441,9 @@ struct OrthoUpdate {
 // A cluster of `cluster` CTAs holds one matrix, each CTA `ks` columns of X
 // (K-major for A = X X^T; the same bytes are the MN-major operand of Q X).
 // Per step: each CTA's part of A goes to the CTAs that own its columns, which
-// add the parts in rank order and hand R and D to all; every CTA forms Q for
-// itself (128^3 is cheaper than an exchange) and updates its own columns.
+// add the parts in rank order and copy their rows of R (columns, by symmetry:
+// whole 128-byte rows) and D to all; every CTA forms Q for itself (128^3 is
+// cheaper than an exchange) and updates its own columns.
 // The products take both halves of their operands (three MMAs for one).
 // Threads: 16 warps; warp w has TMEM lanes 32 (w % 4) .. +31, a row each, and
 // the columns of group w / 4.  Thread 0 issues the MMAs.
@@ -475,7 +476,7 @@ struct OsSmem {
   static constexpr int OFF_D = OFF_R + 65536;
   static constexpr int OFF_E = OFF_D + 512;
   static constexpr int OFF_RED = OFF_E + 512;             // 16 + 8 doubles
-  static constexpr int OFF_BAR = OFF_RED + 192;
+  static constexpr int OFF_BAR = OFF_RED + 192;           // MMAs, received rows
   static constexpr int SMEM_DYN = OFF_BAR + 32 + 1024;
   static_assert(SMEM_DYN <= 232448, "shared memory");
 };
@@ -528,6 +529,14 @@ __device__ __forceinline__ void os_write16(uint8_t* hi, uint8_t* lo, int row, in
   }
 }
 
+// r[at] as a float (0 outside), by selects.
+__device__ __forceinline__ float os_pick(const uint32_t (&r)[16], int at) {
+  uint32_t v = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v = i == at ? r[i] : v;
+  return __uint_as_float(v);
+}
+
 // All writes to shared memory (of this or another CTA) before, all operand
 // reads after.
 __device__ __forceinline__ void os_sync(bool cluster) {
@@ -552,8 +561,9 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
   float* E = reinterpret_cast<float*>(smem + L::OFF_E);
   double* red = reinterpret_cast<double*>(smem + L::OFF_RED);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 16);
+  uint64_t* got = bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 20);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, grp = warp >> 2;
   const int row = 32 * q + lane;
@@ -564,6 +574,7 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
 
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(got, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -587,14 +598,46 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
     return p.tall ? base + static_cast<int64_t>(c0 + c) * p.n + r
                   : base + static_cast<int64_t>(r) * p.k + c0 + c;
   };
-  const int fast = p.tall ? p.n : width;           // neighbours in memory
-  const int count = p.n * width;
+  // Threads take eight neighbours of U at a time: columns of a row of X, or
+  // for a tall U rows of a column.
+  const int fast = p.tall ? p.n : width;
+  const int per = (fast + 7) >> 3;                 // eights in a line
+  const int units = width > 0 ? per * (p.tall ? width : p.n) : 0;
+  const bool vec = ((p.tall ? p.n : p.k) & 7) == 0;  // every eight is whole and aligned
+  auto each = [&](auto&& use) {
+#pragma unroll 2
+    for (int u = tid; u < units; u += kOsThreads) {
+      const int slow = u / per, f = (u - slow * per) * 8;
+      const int r = p.tall ? f : slow, c = p.tall ? slow : f;
+      const int64_t at = u_at(r, c);
+      float v[8];
+      if (!vec) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = f + j < fast ? ortho_load(p.U, p.u_bf16 != 0, at + j) : 0.0f;
+      } else if (p.u_bf16) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.U) + at));
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = bf16_bits_to_f32(ws[j] & 0xFFFFu);
+          v[2 * j + 1] = bf16_bits_to_f32(ws[j] >> 16);
+        }
+      } else {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.U) + at);
+        const float4 x = __ldg(src), y = __ldg(src + 1);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+      }
+      use(r, c, v);
+    }
+  };
   double s = 0.0;
-  for (int i = tid; i < count; i += kOsThreads) {
-    const int slow = i / fast, f = i - slow * fast;
-    const double v = ortho_load(p.U, p.u_bf16 != 0, p.tall ? u_at(f, slow) : u_at(slow, f));
-    s += v * v;
-  }
+  each([&](int, int, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += static_cast<double>(v[j]) * static_cast<double>(v[j]);
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (lane == 0) red[warp] = s;
@@ -621,16 +664,27 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
   s = 0.0;
   for (int i = 0; i < p.cluster; ++i) s += red[16 + i];
   const double norm = sqrt(s) + static_cast<double>(p.eps);
-  const double inv = norm > 0.0 ? 1.0 / norm : 0.0;  // eps = 0 and U = 0: X = 0
-  for (int i = tid; i < count; i += kOsThreads) {
-    const int slow = i / fast, f = i - slow * fast;
-    const int r = p.tall ? f : slow, c = p.tall ? slow : f;
-    uint16_t h, l;
-    split_half(static_cast<float>(ortho_load(p.U, p.u_bf16 != 0, u_at(r, c)) * inv) * p.scale, h,
-               l);
-    *reinterpret_cast<uint16_t*>(Xh + os_at(r, c)) = h;
-    *reinterpret_cast<uint16_t*>(Xl + os_at(r, c)) = l;
-  }
+  // 1 / norm times the scale as power * mantissa * power, each in fp32's range
+  // (eps = 0 and U = 0: X = 0).
+  int e = 0;
+  const float man = norm > 0.0 ? static_cast<float>(frexp(1.0 / norm, &e)) : 0.0f;
+  const float p1 = exp2f(static_cast<float>(e / 2));
+  const float p2 = exp2f(static_cast<float>(e - e / 2)) * p.scale;
+  each([&](int r, int c, const float (&v)[8]) {
+    __align__(16) uint16_t h[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split_half(v[j] * p1 * man * p2, h[j], l[j]);
+    if (!p.tall) {  // (columns past the last one get their zeros again)
+      *reinterpret_cast<uint4*>(Xh + os_at(r, c)) = *reinterpret_cast<const uint4*>(h);
+      *reinterpret_cast<uint4*>(Xl + os_at(r, c)) = *reinterpret_cast<const uint4*>(l);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        *reinterpret_cast<uint16_t*>(Xh + os_at(r + j, c)) = h[j];
+        *reinterpret_cast<uint16_t*>(Xl + os_at(r + j, c)) = l[j];
+      }
+    }
+  });
   os_sync(false);
 
   uint32_t phase = 0;
@@ -675,16 +729,19 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
         tmem_ld_32x32b_x16(lanes + kGramCol + j, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float z = __uint_as_float(r[i]);
-          if (j + i == row) D[row] = z * c.gram_true;
-          v[i] = j + i == row ? 0.0f : z * c.gram_R;
-        }
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) * c.gram_R;
         os_write16(Rh, Rl, row, j, v);
+        const float d = os_pick(r, row - j);
+        if (row >= j && row < j + 16) {  // the diagonal
+          D[row] = d * c.gram_true;
+          *reinterpret_cast<uint16_t*>(Rh + os_at(row, row)) = 0;
+          *reinterpret_cast<uint16_t*>(Rl + os_at(row, row)) = 0;
+        }
       }
       os_sync(false);
     } else {
-      // Part `rank` of columns [share * o, +share) to CTA o: [rank][column][row].
+      // Part `rank` of columns [share * o, +share) to CTA o, four columns of a
+      // row together: [rank][column / 4][row][4].
       const int share = 128 / p.cluster;
 #pragma unroll 1
       for (int j = 32 * grp; j < 32 * grp + 32; j += 16) {
@@ -694,54 +751,80 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
         const uint32_t owner = static_cast<uint32_t>(j / share);  // 16 columns, one owner
         const uint32_t at = map_to_rank(
             smem_u32(Rh) + static_cast<uint32_t>(
-                               ((static_cast<int>(rank) * share + j % share) * 128 + row) * 4),
+                               ((static_cast<int>(rank) * share + j % share) * 32 + row) * 16),
             owner);
+        // (column / 4) * 128 rows * 16 bytes = column * 512: 128 * 4 bytes a column
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + i * 512), "r"(r[i])
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 2048),
+                       "r"(r[4 * i]), "r"(r[4 * i + 1]), "r"(r[4 * i + 2]), "r"(r[4 * i + 3])
                        : "memory");
       }
       os_sync(true);
       // The sums of this CTA's columns, in rank order; thread (row, grp) has
       // share / 4 of them.
       const int mine = share / 4, first = grp * mine;
-      const float* parts = reinterpret_cast<const float*>(Rh);
+      const float4* parts = reinterpret_cast<const float4*>(Rh);
       float sum[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        sum[i] = 0.0f;
-        if (i < mine) {
-          float v = parts[(first + i) * 128 + row];
-          for (int o = 1; o < p.cluster; ++o)
-            v = __fadd_rn(v, parts[(o * share + first + i) * 128 + row]);
-          sum[i] = v;
-        }
-      }
-      os_sync(true);  // the parts were read everywhere: R may take their place
-      for (int o = 0; o < p.cluster; ++o) {
-        const uint32_t h_base = map_to_rank(smem_u32(Rh), o), l_base = map_to_rank(smem_u32(Rl), o);
-        const uint32_t d_base = map_to_rank(smem_u32(D), o);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < mine) {
-            const int col = static_cast<int>(rank) * share + first + i;
-            if (col == row)
-              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(d_base + 4 * row),
-                           "f"(sum[i] * c.gram_true)
-                           : "memory");
-            uint16_t h, l;
-            split_half(col == row ? 0.0f : sum[i] * c.gram_R, h, l);
-            // R is symmetric: (col, row), so that lanes are neighbours
-            const uint32_t at = static_cast<uint32_t>(os_at(col, row));
-            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(h_base + at), "h"(h) : "memory");
-            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(l_base + at), "h"(l) : "memory");
+      for (int i = 0; i < 4; ++i) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (4 * i < mine) {
+          v = parts[((first >> 2) + i) * 128 + row];
+          for (int o = 1; o < p.cluster; ++o) {
+            const float4 w = parts[(((o * share + first) >> 2) + i) * 128 + row];
+            v.x = __fadd_rn(v.x, w.x);
+            v.y = __fadd_rn(v.y, w.y);
+            v.z = __fadd_rn(v.z, w.z);
+            v.w = __fadd_rn(v.w, w.w);
           }
+        }
+        sum[4 * i] = v.x;
+        sum[4 * i + 1] = v.y;
+        sum[4 * i + 2] = v.z;
+        sum[4 * i + 3] = v.w;
       }
-      os_sync(true);
+      // The rows that the other CTAs send: [share o, +share) of both blocks,
+      // both halves, and of D.
+      if (tid == 0)
+        mbar_arrive_expect_tx(got, static_cast<uint32_t>((p.cluster - 1) * share * (4 * 128 + 4)));
+      os_sync(true);  // the parts were read everywhere: R may take their place
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < mine) {
+          const int col = static_cast<int>(rank) * share + first + i;
+          uint16_t h, l;
+          split_half(col == row ? 0.0f : sum[i] * c.gram_R, h, l);
+          // R is symmetric: (col, row), so that lanes are neighbours
+          const int at = os_at(col, row);
+          *reinterpret_cast<uint16_t*>(Rh + at) = h;
+          *reinterpret_cast<uint16_t*>(Rl + at) = l;
+          if (col == row) D[row] = sum[i] * c.gram_true;
+        }
+      os_sync(false);
+      if (tid < p.cluster && tid != static_cast<int>(rank)) {
+        const uint32_t o = static_cast<uint32_t>(tid), there = map_to_rank(smem_u32(got), o);
+        const uint32_t bytes = static_cast<uint32_t>(share) * 128u;
+        const uint32_t at = smem_u32(Rh) + rank * bytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // blocks 0, 1 of the high half, then of the low
+          dsmem_copy(map_to_rank(at + i * 16384u, o), at + i * 16384u, bytes, there);
+        const uint32_t d = smem_u32(D) + rank * static_cast<uint32_t>(share) * 4u;
+        dsmem_copy(map_to_rank(d, o), d, static_cast<uint32_t>(share) * 4u, there);
+      }
+      if (*abort_flag == 0 && !mbar_wait_bounded(got, it & 1, abort_flag, p.wait_limit_ns)) {
+        *abort_flag = 1;
+        record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
+      }
+      __syncwarp();
+      os_sync(true);  // every copy has arrived: Q may take R's place
     }
     // R R, and Q and a + E in its place
     if (tid == 0) issue(kPolyCol, Rh, Rl, Rh, Rl, 8, false, sq_desc);
     const float di = D[row];
+    const float kr = c.c * c.poly_true * c.to_Q;
+    const float kd = c.c * c.r_true * c.to_Q;
+    const float ki = __fmaf_rn(c.c, di, c.b) * c.r_true * c.to_Q;
     wait_mma();
 #pragma unroll 1
     for (int j = 32 * grp; j < 32 * grp + 32; j += 16) {
@@ -751,22 +834,29 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
       os_read16(Rh, Rl, row, j, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float rr = __uint_as_float(r[i]) * c.poly_true;
-        const float x = v[i] * c.r_true;
-        if (j + i == row) E[row] = c.a + __fmaf_rn(c.c, __fmaf_rn(di, di, rr), c.b * di);
-        v[i] = j + i == row
-                   ? 0.0f
-                   : __fmaf_rn(c.c, __fmaf_rn(di + D[j + i], x, rr), c.b * x) * c.to_Q;
+      for (int i = 0; i < 16; i += 4) {
+        const float4 d4 = *reinterpret_cast<const float4*>(D + j + i);
+        const float dj[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h)  // to_Q (c R R + (b + c (D_i + D_j)) R)
+          v[i + h] = __fmaf_rn(__fmaf_rn(kd, dj[h], ki), v[i + h],
+                               __uint_as_float(r[i + h]) * kr);
       }
       os_write16(Rh, Rl, row, j, v);
+      const float rr = os_pick(r, row - j) * c.poly_true;
+      if (row >= j && row < j + 16) {  // the diagonal
+        E[row] = c.a + __fmaf_rn(c.c, __fmaf_rn(di, di, rr), c.b * di);
+        *reinterpret_cast<uint16_t*>(Rh + os_at(row, row)) = 0;
+        *reinterpret_cast<uint16_t*>(Rl + os_at(row, row)) = 0;
+      }
     }
     os_sync(false);
     // X <- E X + Q X
     if (tid == 0) issue(kUpdCol, Rh, Rl, Xh, Xl, 8, true, upd_desc);
-    const float ei = E[row] * c.x_true;
-    wait_mma();
     const bool last = it == p.steps - 1;
+    const float to = last ? 1.0f : c.to_Y;
+    const float ei = E[row] * c.x_true * to, ku = c.upd_true * to;
+    wait_mma();
     const int quarter = p.ks / 4;
 #pragma unroll 1
     for (int j = quarter * grp; j < quarter * grp + quarter; j += 16) {
@@ -777,10 +867,8 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        v[i] = __fmaf_rn(ei, v[i], __uint_as_float(r[i]) * c.upd_true);
+        v[i] = __fmaf_rn(ei, v[i], __uint_as_float(r[i]) * ku);
       if (!last) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= c.to_Y;
         os_write16(Xh, Xl, row, j, v);
       } else if (row < p.n) {
         if (!p.tall && (p.k & 7) == 0 && j + 16 <= width) {
