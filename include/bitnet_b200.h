@@ -482,12 +482,15 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
  *   z = x W^T;  lse_m = log sum_v exp(z_mv);  loss_m = lse_m - z_m,targets[m]
  *   g_mv = dloss_m (exp(z_mv - lse_m) - [v = targets[m]]);  dx = g W;  dW = g^T x
  * A target outside [0, V) (the usual -100, say) marks a token without loss:
- * loss_m = 0 and the row of g is 0 whatever x holds; lse_m is still written.
+ * loss_m = 0 and the row of g is 0; lse_m is still written.  (In dW = g^T x a
+ * 0 times a non-finite x is NaN all the same.)
  *
  *   x [M][K], W [V][K] bf16; targets [M] int64; loss, lse, dloss [M] fp32;
  *   dx [M][K], dW [V][K] bf16, either may be NULL (not computed).
- *   All sums and the softmax's maximum, sum and logarithm are fp32; g is
- *   rounded to bf16 as an operand of the two gradient products.
+ *   All sums and the softmax's maximum, sum and logarithm are fp32; loss is
+ *   log(1 + sum over the others of exp(z_v - z_t)), so a confident token's
+ *   keeps its digits; g / max|dloss| is rounded to bf16 as an operand of the
+ *   two gradient products.
  *   Non-finite logits of a row give a non-finite or NaN lse and loss.
  *   M == 0: the forward queues nothing, the backward zeroes dW.
  * Shapes: K % 8 == 0, 8 <= K <= BITNET_MAX_K, 1 <= V <= BITNET_MAX_N,
@@ -524,13 +527,15 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void *x, const void
  *   coefficients host array of 3 * steps doubles: a, b, c of each step.
  *   O            [B][N][K] bf16 out; must not overlap U.
  *   X is held in 22 bits, A's and b A + c A A's diagonals in fp32, sums in
- *   fp32; the products' operands are fp16.  A non-finite entry makes its
- *   matrix NaN, a zero matrix gives zeros (eps 0 included).
+ *   fp32; the products' operands are fp16, for min(N, K) <= 192 in both
+ *   halves (22 bits).  A non-finite entry makes its matrix NaN, a zero matrix
+ *   gives zeros (eps 0 included).
  * 1 <= steps <= 32, eps >= 0; the coefficients finite and such that no step
  * takes singular values of at most 1 beyond 2^20 (BITNET_ERR_INVALID_ARG).
  * Shapes: 1 <= N, K <= BITNET_MAX_K, 0 <= B <= 65535, at most 2^30 tiles of
- * 128 x 128 in all.  U, O 16-byte aligned; workspace >= the size query,
- * 256-byte aligned, contents on entry irrelevant; one per call in flight.
+ * 128 x 128 in all.  U, O 16-byte aligned; workspace >= the size query (0,
+ * and NULL allowed, for updates of up to 128 x 2048 or 2048 x 128), 256-byte
+ * aligned, contents on entry irrelevant; one per call in flight.
  * The same input gives the same bits on every call.
  * ---------------------------------------------------------------------- */
 BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K);

@@ -846,9 +846,10 @@ def bitnet_orthogonalize(U, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, ep
     rows = list(coefficients)
     if len(rows) == 3 and all(isinstance(c, (int, float)) for c in rows):
         rows = [rows] * steps
-    flat = [float(c) for row in rows for c in row]
-    if len(rows) != steps or len(flat) != 3 * steps or any(len(row) != 3 for row in rows):
+    if len(rows) != steps or any(not isinstance(row, (list, tuple)) or len(row) != 3
+                                 for row in rows):
         raise ValueError("coefficients must be (a, b, c), or one such triple for each step")
+    flat = [float(c) for row in rows for c in row]
     if out is not None:
         _expect(out, "out", torch.bfloat16, shape=tuple(U.shape))
     lib = load_library()

@@ -345,7 +345,7 @@ CeBwdLayout ce_bwd_layout(int64_t M, int64_t V, int64_t K) {
 
 constexpr int kOrthoMaxSteps = 32;
 // Largest smaller side that runs on both halves of its operands.
-constexpr int64_t kOrthoSplitN = 256;
+constexpr int64_t kOrthoSplitN = 192;
 
 // Updates that run in one launch on clusters of up to eight CTAs.
 bool ortho_is_small(int64_t N, int64_t K) {
