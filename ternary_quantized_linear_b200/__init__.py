@@ -8,7 +8,6 @@ CUDA kernels; PyTorch only provides device memory and streams.  There is no
 CPU fallback: if the library is missing or a call fails, an exception is
 raised.
 """
-import contextlib
 import ctypes
 import os
 import threading
@@ -727,19 +726,20 @@ def bitnet_bitdelta_forward(x, W_base, signs, alpha, y_dtype=torch.float32, y=No
     return y
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Run on `device` and on `stream` (the device's current one when None):
-    memory allocated inside belongs to the stream the kernels run on, so a
-    buffer freed on return is not handed to another stream's work."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-            with torch.cuda.stream(stream):
-                yield
+def _on(device, stream, run):
+    """run(handle) on `device` and on `stream` (the device's current one when
+    None), handle being the stream's pointer: memory allocated inside belongs
+    to the stream the kernels run on, so a buffer freed on return is not
+    handed to another stream's work."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return run(ctypes.c_void_p(torch.cuda.current_stream(device.index).cuda_stream))
+        with torch.cuda.device(device):
+            return run(_stream())
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return run(_stream(stream))
 
 
 def _same_device(first, *ts):
@@ -780,16 +780,18 @@ def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=N
         _expect(workspace, "workspace", torch.uint8, numel=nb)
     _need_cuda(x, W, targets, loss, lse, workspace)
     _same_device(x, W, targets, loss, lse, workspace)
-    with _on(x.device, stream):
-        if loss is None:
-            loss = torch.empty((M,), dtype=torch.float32, device=x.device)
-        if lse is None:
-            lse = torch.empty((M,), dtype=torch.float32, device=x.device)
-        ws = _scratch(workspace, nb, x.device)
+    dev = x.device
+
+    def run(handle):
+        y = torch.empty((M,), dtype=torch.float32, device=dev) if loss is None else loss
+        z = torch.empty((M,), dtype=torch.float32, device=dev) if lse is None else lse
+        ws = _scratch(workspace, nb, dev)
         _check("bitnet_cross_entropy_forward", lib.bitnet_cross_entropy_forward(
-            _ptr(x), _ptr(W), _ptr(targets), M, V, K, _ptr(loss), _ptr(lse), _ptr(ws),
-            ws.numel(), _stream()))
-    return loss, lse
+            _ptr(x), _ptr(W), _ptr(targets), M, V, K, _ptr(y), _ptr(z), _ptr(ws), ws.numel(),
+            handle))
+        return y, z
+
+    return _on(dev, stream, run)
 
 
 def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_dW=True, dx=None,
@@ -811,17 +813,21 @@ def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_
         _expect(workspace, "workspace", torch.uint8, numel=nb)
     _need_cuda(x, W, targets, lse, dloss, dx, dW, workspace)
     _same_device(x, W, targets, lse, dloss, dx, dW, workspace)
-    with _on(x.device, stream):
-        if dx is None and need_dx:
-            dx = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-        if dW is None and need_dW:
-            dW = torch.empty((V, K), dtype=torch.bfloat16, device=x.device)
-        dx, dW = dx if need_dx else None, dW if need_dW else None
-        ws = _scratch(workspace, nb, x.device)
+    dev = x.device
+
+    def run(handle):
+        gx, gW = dx if need_dx else None, dW if need_dW else None
+        if gx is None and need_dx:
+            gx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        if gW is None and need_dW:
+            gW = torch.empty((V, K), dtype=torch.bfloat16, device=dev)
+        ws = _scratch(workspace, nb, dev)
         _check("bitnet_cross_entropy_backward", lib.bitnet_cross_entropy_backward(
-            _ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K, _ptr(dx), _ptr(dW),
-            _ptr(ws), ws.numel(), _stream()))
-    return dx, dW
+            _ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K, _ptr(gx), _ptr(gW),
+            _ptr(ws), ws.numel(), handle))
+        return gx, gW
+
+    return _on(dev, stream, run)
 
 
 # Coefficients a, b, c of the quintic step that bitnet_orthogonalize takes by
@@ -858,15 +864,17 @@ def bitnet_orthogonalize(U, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, ep
         _expect(workspace, "workspace", torch.uint8, numel=nb)
     _need_cuda(U, out, workspace)
     _same_device(U, out, workspace)
-    with _on(U.device, stream):
-        if out is None:
-            out = torch.empty(tuple(U.shape), dtype=torch.bfloat16, device=U.device)
-        ws = _scratch(workspace, nb, U.device)
+    dev = U.device
+
+    def run(handle):
+        O = torch.empty(tuple(U.shape), dtype=torch.bfloat16, device=dev) if out is None else out
+        ws = _scratch(workspace, nb, dev)
         _check("bitnet_orthogonalize", lib.bitnet_orthogonalize(
-            _ptr(U), _dtype_code(U.dtype), B, N, K, steps,
-            (ctypes.c_double * (3 * steps))(*flat), ctypes.c_float(eps), _ptr(out), _ptr(ws),
-            ws.numel(), _stream()))
-    return out
+            _ptr(U), _dtype_code(U.dtype), B, N, K, steps, (ctypes.c_double * (3 * steps))(*flat),
+            ctypes.c_float(eps), _ptr(O), _ptr(ws), ws.numel(), handle))
+        return O
+
+    return _on(dev, stream, run)
 
 
 def _weights_ptr_layout(W, K):

@@ -415,10 +415,11 @@ struct TgInput {
   }
 };
 
-// The block for the next output of an Epi with two slots and no inputs.
+// The block for the next output of an Epi without inputs: the store before
+// the last kSlots - 1 has been read out.
 template <class Epi>
 __device__ __forceinline__ uint8_t* tg_out_block(TgStage& st) {
-  if (st.lane == 0) bulk_wait_read<1>();
+  if (st.lane == 0) bulk_wait_read<Epi::kSlots - 1>();
   __syncwarp();
   return st.base + (st.seq++ % Epi::kSlots) * Epi::kSlotBytes;
 }
@@ -770,7 +771,7 @@ __device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensor
 
 // D to bf16, times a device scalar when given.
 struct TgStoreBf16 {
-  static constexpr int kSlots = 2, kSlotBytes = 2048;
+  static constexpr int kSlots = 4, kSlotBytes = 2048;
   struct Params {
     const float* scale;
   };
