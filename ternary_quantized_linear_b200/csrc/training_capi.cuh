@@ -99,9 +99,9 @@ int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) 
 
 // Cycles that a plan needs, roughly: its waves of tiles, a tile's steps and
 // its epilogue.  A pair's 64-k step takes 660 cycles (measured; the MMAs
-// alone 512), a 128 x 128 step 600 (32 KiB at 64 bytes a cycle are 512; the
+// alone 512), a 128 x 128 step 680 (32 KiB at 64 bytes a cycle are 512; the
 // MMAs 256); the epilogue and what a launch waits for come on top of each
-// wave, and for a cluster's split the meeting of the parts.  Of clusters of
+// wave, and for a cluster's split the meeting of the parts (3 us).  Of clusters of
 // two SMs 74 are resident at a time, of four 33 (the occupancy query's answer
 // on a B200: its SM groups do not divide into fours).
 double tg_cost(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, const TgPlan& pl) {
@@ -109,8 +109,8 @@ double tg_cost(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, con
   const int64_t slots = pl.split == 4 ? 33 : kPlanSms / std::max(pl.cg, pl.split);
   const double waves = static_cast<double>(ceil_div(tiles, slots));
   if (pl.cg == 2) return waves * (660.0 * static_cast<double>(steps) + 5000.0);
-  return waves * (600.0 * static_cast<double>(ceil_div(steps, pl.split)) + 3000.0 +
-                  (pl.split > 1 ? 1500.0 : 0.0));
+  return waves * (680.0 * static_cast<double>(ceil_div(steps, pl.split)) + 3000.0 +
+                  (pl.split > 1 ? 5500.0 : 0.0));
 }
 
 // Pairs on 256 x 256 tiles, or single SMs on 128 x 128 tiles, each tile's
