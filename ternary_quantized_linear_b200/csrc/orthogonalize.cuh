@@ -48,35 +48,87 @@ __device__ __forceinline__ float ortho_load(const void* U, bool bf16, int64_t i)
               : static_cast<const float*>(U)[i];
 }
 
+// Eight entries of U from `at` on, the first `n` of them (0 beyond); vec: all
+// eight, 16-byte aligned.
+__device__ __forceinline__ void ortho_load8(const void* U, bool bf16, int64_t at, bool vec, int n,
+                                            float (&v)[8]) {
+  if (!vec) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? ortho_load(U, bf16, at + j) : 0.0f;
+  } else if (bf16) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(U) + at));
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_bits_to_f32(ws[j] & 0xFFFFu);
+      v[2 * j + 1] = bf16_bits_to_f32(ws[j] >> 16);
+    }
+  } else {
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(U) + at);
+    const float4 x = __ldg(src), y = __ldg(src + 1);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+  }
+}
+
+__device__ __forceinline__ double ortho_squares(const float (&v)[8]) {
+  double s = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s += static_cast<double>(v[j]) * static_cast<double>(v[j]);
+  return s;
+}
+
+// scale / norm as power * mantissa * power, each within fp32's range, so that
+// updates far from 1 keep their digits; norm = 0 (eps = 0 and U = 0): 0.
+struct OrthoFactor {
+  float p1, man, p2;
+  __device__ __forceinline__ float operator()(float v) const { return v * p1 * man * p2; }
+};
+
+__device__ __forceinline__ OrthoFactor ortho_factor(double norm, float scale) {
+  int e = 0;
+  const float man = norm > 0.0 ? static_cast<float>(frexp(1.0 / norm, &e)) : 0.0f;
+  return OrthoFactor{exp2f(static_cast<float>(e / 2)), man,
+                     exp2f(static_cast<float>(e - e / 2)) * scale};
+}
+
 // Sum of squares of one block's share of a matrix, in fp64 (the squares of
-// fp32 values neither overflow nor vanish there), in a fixed order.
+// fp32 values neither overflow nor vanish there), in a fixed order.  vec: the
+// matrices' sizes are multiples of 8.
 __global__ void __launch_bounds__(kOrthoNormThreads)
-ortho_norm_kernel(const void* __restrict__ U, int u_bf16, int64_t size,
+ortho_norm_kernel(const void* __restrict__ U, int u_bf16, int64_t size, int vec,
                   double* __restrict__ part) {
-  __shared__ double red[kOrthoNormThreads];
+  __shared__ double red[kOrthoNormThreads / 32];
   const int64_t base = static_cast<int64_t>(blockIdx.y) * size;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   double s = 0.0;
+  const int64_t eights = (size + 7) >> 3;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kOrthoNormThreads;
   const int64_t me = blockIdx.x * static_cast<int64_t>(kOrthoNormThreads) + threadIdx.x;
-  for (int64_t i = me; i < size; i += step) {
-    const double v = ortho_load(U, u_bf16 != 0, base + i);
-    s += v * v;
+#pragma unroll 4
+  for (int64_t i = me; i < eights; i += step) {
+    float v[8];
+    ortho_load8(U, u_bf16 != 0, base + 8 * i, vec != 0,
+                static_cast<int>(min(static_cast<int64_t>(8), size - 8 * i)), v);
+    s += ortho_squares(v);
   }
-  red[threadIdx.x] = s;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
-  for (int h = kOrthoNormThreads / 2; h > 0; h >>= 1) {
-    if (threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
-    __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int i = 0; i < kOrthoNormThreads / 32; ++i) s += red[i];
+    part[blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x] = s;
   }
-  if (threadIdx.x == 0) part[blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x] = red[0];
 }
 
-// 1 / (||U||_F + eps) of matrix b from the blocks' sums, in a fixed order;
-// all 256 threads of a block.
-__device__ __forceinline__ double ortho_inverse_norm(const double* part, int parts, int b,
-                                                     float eps, double* red) {
+// ||U||_F + eps of matrix b from the blocks' sums, in a fixed order; all 256
+// threads of a block.
+__device__ __forceinline__ double ortho_norm_of(const double* part, int parts, int b, float eps,
+                                                double* red) {
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += 256)
     s += __ldcg(part + static_cast<int64_t>(b) * parts + i);
@@ -85,13 +137,12 @@ __device__ __forceinline__ double ortho_inverse_norm(const double* part, int par
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
   s = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
-  const double norm = sqrt(s) + static_cast<double>(eps);
-  return norm > 0.0 ? 1.0 / norm : 0.0;  // eps = 0 and U = 0: X = 0
+  return sqrt(s) + static_cast<double>(eps);
 }
 
 // X = U / (||U||_F + eps) times `scale`, as two halves, [n][ldx], from a wide
-// U [n][k]: eight elements per thread and round (U's rows 16-byte aligned when
-// `vec`; the last columns of a row may be padding of X).
+// U [n][k]: a block takes rows, a thread eight entries at a time (U's rows
+// 16-byte aligned when `vec`; the last columns of a row may be padding of X).
 __global__ void __launch_bounds__(256)
 ortho_start_kernel(const void* __restrict__ U, int u_bf16, int64_t n, int64_t k, int vec,
                    const double* __restrict__ part, int parts, float eps, float scale,
@@ -100,39 +151,21 @@ ortho_start_kernel(const void* __restrict__ U, int u_bf16, int64_t n, int64_t k,
   const int b = blockIdx.y;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const double inv = ortho_inverse_norm(part, parts, b, eps, red);
-  const int64_t per_row = (k + 7) >> 3, total = n * per_row;
-  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
-    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-    const int64_t at = (static_cast<int64_t>(b) * n + r) * k + c;
-    float v[8];
-    if (vec) {
-      if (u_bf16) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(U) + at));
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  const OrthoFactor f = ortho_factor(ortho_norm_of(part, parts, b, eps, red), scale);
+  for (int64_t r = blockIdx.x; r < n; r += gridDim.x) {
+    const int64_t from = (static_cast<int64_t>(b) * n + r) * k;
+    const int64_t to = (static_cast<int64_t>(b) * n + r) * ldx;
+#pragma unroll 2
+    for (int64_t c = 8 * threadIdx.x; c < k; c += 8 * 256) {
+      float v[8];
+      ortho_load8(U, u_bf16 != 0, from + c, vec != 0,
+                  static_cast<int>(min(static_cast<int64_t>(8), k - c)), v);
+      __align__(16) uint16_t h[8], l[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[2 * j] = bf16_bits_to_f32(ws[j] & 0xFFFFu);
-          v[2 * j + 1] = bf16_bits_to_f32(ws[j] >> 16);
-        }
-      } else {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(U) + at);
-        const float4 x = __ldg(s), y = __ldg(s + 1);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = c + j < k ? ortho_load(U, u_bf16 != 0, at + j) : 0.0f;
+      for (int j = 0; j < 8; ++j) split_half(f(v[j]), h[j], l[j]);
+      *reinterpret_cast<uint4*>(hi + to + c) = *reinterpret_cast<const uint4*>(h);
+      *reinterpret_cast<uint4*>(lo + to + c) = *reinterpret_cast<const uint4*>(l);
     }
-    __align__(16) uint16_t h[8], l[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      split_half(static_cast<float>(v[j] * inv) * scale, h[j], l[j]);
-    const int64_t o = (static_cast<int64_t>(b) * n + r) * ldx + c;
-    *reinterpret_cast<uint4*>(hi + o) = *reinterpret_cast<const uint4*>(h);
-    *reinterpret_cast<uint4*>(lo + o) = *reinterpret_cast<const uint4*>(l);
   }
 }
 
@@ -147,7 +180,7 @@ ortho_start_tall_kernel(const void* __restrict__ U, int u_bf16, int rows, int co
   const int b = blockIdx.z;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const double inv = ortho_inverse_norm(part, parts, b, eps, red);
+  const OrthoFactor f = ortho_factor(ortho_norm_of(part, parts, b, eps, red), scale);
   const int64_t base = static_cast<int64_t>(b) * rows * cols;
   const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 32;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -164,8 +197,8 @@ ortho_start_tall_kernel(const void* __restrict__ U, int u_bf16, int rows, int co
     const int c = c0 + i, r = r0 + 2 * tx;
     if (c < cols && r < rows) {  // rows past the last one are padding of X
       uint16_t h[2], l[2];
-      split_half(static_cast<float>(tile[i][2 * tx] * inv) * scale, h[0], l[0]);
-      split_half(static_cast<float>(tile[i][2 * tx + 1] * inv) * scale, h[1], l[1]);
+      split_half(f(tile[i][2 * tx]), h[0], l[0]);
+      split_half(f(tile[i][2 * tx + 1]), h[1], l[1]);
       const int64_t o = (static_cast<int64_t>(b) * cols + c) * ldx + r;
       *reinterpret_cast<uint32_t*>(hi + o) = h[0] | (static_cast<uint32_t>(h[1]) << 16);
       *reinterpret_cast<uint32_t*>(lo + o) = l[0] | (static_cast<uint32_t>(l[1]) << 16);
@@ -611,33 +644,12 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
       const int r = p.tall ? f : slow, c = p.tall ? slow : f;
       const int64_t at = u_at(r, c);
       float v[8];
-      if (!vec) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] = f + j < fast ? ortho_load(p.U, p.u_bf16 != 0, at + j) : 0.0f;
-      } else if (p.u_bf16) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(p.U) + at));
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[2 * j] = bf16_bits_to_f32(ws[j] & 0xFFFFu);
-          v[2 * j + 1] = bf16_bits_to_f32(ws[j] >> 16);
-        }
-      } else {
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.U) + at);
-        const float4 x = __ldg(src), y = __ldg(src + 1);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-      }
+      ortho_load8(p.U, p.u_bf16 != 0, at, vec, fast - f, v);
       use(r, c, v);
     }
   };
   double s = 0.0;
-  each([&](int, int, const float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += static_cast<double>(v[j]) * static_cast<double>(v[j]);
-  });
+  each([&](int, int, const float (&v)[8]) { s += ortho_squares(v); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (lane == 0) red[warp] = s;
@@ -663,17 +675,11 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
   os_sync(many);
   s = 0.0;
   for (int i = 0; i < p.cluster; ++i) s += red[16 + i];
-  const double norm = sqrt(s) + static_cast<double>(p.eps);
-  // 1 / norm times the scale as power * mantissa * power, each in fp32's range
-  // (eps = 0 and U = 0: X = 0).
-  int e = 0;
-  const float man = norm > 0.0 ? static_cast<float>(frexp(1.0 / norm, &e)) : 0.0f;
-  const float p1 = exp2f(static_cast<float>(e / 2));
-  const float p2 = exp2f(static_cast<float>(e - e / 2)) * p.scale;
+  const OrthoFactor factor = ortho_factor(sqrt(s) + static_cast<double>(p.eps), p.scale);
   each([&](int r, int c, const float (&v)[8]) {
     __align__(16) uint16_t h[8], l[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) split_half(v[j] * p1 * man * p2, h[j], l[j]);
+    for (int j = 0; j < 8; ++j) split_half(factor(v[j]), h[j], l[j]);
     if (!p.tall) {  // (columns past the last one get their zeros again)
       *reinterpret_cast<uint4*>(Xh + os_at(r, c)) = *reinterpret_cast<const uint4*>(h);
       *reinterpret_cast<uint4*>(Xl + os_at(r, c)) = *reinterpret_cast<const uint4*>(l);

@@ -106,11 +106,24 @@ __device__ __forceinline__ TgTile tg_tile(const TgShape& p, int t) {
   o.b = t / p.per_batch;
   const int r = t - o.b * p.per_batch;
   if (p.sym) {
-    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-    while (static_cast<int64_t>(i + 1) * (i + 2) / 2 <= r) ++i;
-    while (static_cast<int64_t>(i) * (i + 1) / 2 > r) --i;
-    o.m = i;
-    o.n = r - static_cast<int>(static_cast<int64_t>(i) * (i + 1) / 2);
+    // Bands of 8 tile rows; a band is swept over n with m fastest (its square
+    // part, then the triangle on the diagonal), so that tiles under way
+    // together share rows of both operands.  Before band t: 32 t^2 + 4 t.
+    int t8 = static_cast<int>((sqrtf(16.0f + 128.0f * static_cast<float>(r)) - 4.0f) / 64.0f);
+    while (static_cast<int64_t>(t8 + 1) * (32LL * (t8 + 1) + 4) <= r) ++t8;
+    while (static_cast<int64_t>(t8) * (32LL * t8 + 4) > r) --t8;
+    const int first = 8 * t8, rows = min(8, p.mt - first);
+    int w = r - static_cast<int>(static_cast<int64_t>(t8) * (32LL * t8 + 4));
+    if (w < rows * first) {
+      o.n = w / rows;
+      o.m = first + (w - o.n * rows);
+    } else {
+      w -= rows * first;
+      int i = 0;
+      while (w > i) w -= ++i;  // row i of the triangle has i + 1 tiles
+      o.m = first + i;
+      o.n = first + w;
+    }
   } else {
     // m varies fastest inside a group of `group` tile rows: B's tile stays
     // in L2 for all of them, A's group for the whole sweep.

@@ -195,7 +195,11 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   p.split_steps = static_cast<int>(ceil_div(p.steps, SPLIT > 1 ? SPLIT : g.ksplit));
   p.ksplit = g.ksplit;
   p.tiles = static_cast<int>(g.batch * p.per_batch * p.ksplit);
-  p.group = 8;
+  // Tile rows that share a sweep over n: 8, or up to 16 while their rows of A
+  // stay within 32 MiB of L2 (8192 tokens over 128000 x 4096: 8 rows 7.02 ms,
+  // 16 6.79, 32 7.25).
+  p.group = static_cast<int>(std::max<int64_t>(
+      8, std::min<int64_t>(16, (32LL << 20) / (128LL * CG * 2 * g.Kc))));
   p.passes = g.passes;
   p.a_mn = g.a.mn ? 1 : 0;
   p.b_mn = g.b.mn ? 1 : 0;
@@ -719,7 +723,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
 
   st = launch_pdl(ortho_norm_kernel,
                   dim3(static_cast<unsigned>(L.parts), static_cast<unsigned>(B)),
-                  kOrthoNormThreads, s, U, u_bf16, N * K, norm);
+                  kOrthoNormThreads, s, U, u_bf16, N * K, N * K % 8 == 0 ? 1 : 0, norm);
   if (st != BITNET_OK) return st;
   double sx = fp16_scale(top[0]);
   if (tall) {
@@ -729,8 +733,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
                     256, s, U, u_bf16, static_cast<int>(N), static_cast<int>(K), norm, L.parts,
                     eps, static_cast<float>(sx), half_at(L.X[0]), half_at(L.X_lo[0]), L.ldx);
   } else {
-    const int64_t work = ceil_div(N * ceil_div(K, 8), 256);
-    const int64_t blocks = std::min<int64_t>(work, std::max<int64_t>(1, 16LL * ds->num_sms / B));
+    const int64_t blocks = std::min<int64_t>(N, std::max<int64_t>(1, 16LL * ds->num_sms / B));
     st = launch_pdl(ortho_start_kernel,
                     dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(B)), 256, s, U,
                     u_bf16, N, K, K % 8 == 0 ? 1 : 0, norm, L.parts, eps, static_cast<float>(sx),
