@@ -120,61 +120,101 @@ struct CeStats {
   }
 };
 
-// Joins the parts of each row: 32 rows x 32 lanes of parts per block (parts
-// of neighbouring rows are neighbours in memory); warp w also forms the
-// target's logit of row w.
-__global__ void __launch_bounds__(1024)
+// The statistics (maximum, sum) of two sets of entries as those of both.
+__device__ __forceinline__ void ce_join(float& mx, float& sum, float pm, float ps) {
+  const float m_new = fmaxf(mx, pm);
+  if (m_new != -INFINITY) {
+    sum = __fmaf_rn(sum, exp2_approx((mx - m_new) * kLog2e),
+                    ps * exp2_approx((pm - m_new) * kLog2e));
+    mx = m_new;
+  } else {
+    sum += ps;  // 0, or NaN
+  }
+}
+
+// Loss and lse of a row from the statistics of all entries but the target's.
+__device__ __forceinline__ void ce_finish(float mx, float sum, bool valid, float z, float* loss,
+                                          float* lse) {
+  if (!valid) {
+    *loss = 0.0f;
+    *lse = mx + logf(sum);
+    return;
+  }
+  const float d = mx - z;  // loss = log(1 + sum exp(mx - z))
+  float l;
+  if (mx == -INFINITY && sum == 0.0f)
+    l = z - z;  // no other entry with any weight (NaN for a non-finite z)
+  else
+    l = d <= 0.0f ? log1pf(sum * expf(d)) : d + logf(sum + expf(-d));
+  *loss = l;
+  *lse = z + l;
+}
+
+// Joins the parts of each row.  kWide (many rows): 32 rows x 32 lanes of parts
+// per block, neighbouring rows' parts being neighbours in memory; warp w also
+// forms the target's logit of row w.  Else a block of 8 warps per row, its
+// threads over the parts: one token's 286 parts were 9 dependent loads and 31
+// dependent joins with the other cut (8 us; 4 with this one).  The target's
+// logit depends on the inputs alone and is formed while the product runs.
+template <bool kWide>
+__global__ void __launch_bounds__(kWide ? 1024 : 256)
 ce_join_kernel(const float2* __restrict__ part, int parts, const __nv_bfloat16* __restrict__ x,
                const __nv_bfloat16* __restrict__ W, const int64_t* __restrict__ targets,
                int64_t V, int64_t K, int M, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float smx[32][33], ssum[32][33], slogit[32];
-  const int r = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 32 + r;
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
-  {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + w;
-    const int64_t t = row < M ? targets[row] : -1;
-    float z = 0.0f;
-    if (t >= 0 && t < V) z = ce_target_dot(x + row * K, W + t * K, K, r);
-    if (r == 0) slogit[w] = z;
-  }
-  float mx = -INFINITY, sum = 0.0f;
-  auto join = [&](float pm, float ps) {
-    const float m_new = fmaxf(mx, pm);
-    if (m_new != -INFINITY) {
-      sum = __fmaf_rn(sum, exp2_approx((mx - m_new) * kLog2e),
-                      ps * exp2_approx((pm - m_new) * kLog2e));
-      mx = m_new;
-    } else {
-      sum += ps;  // 0, or NaN
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if constexpr (kWide) {
+    __shared__ float smx[32][33], ssum[32][33], slogit[32];
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    {
+      const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + w;
+      const int64_t t = row < M ? targets[row] : -1;
+      float z = 0.0f;
+      if (t >= 0 && t < V) z = ce_target_dot(x + row * K, W + t * K, K, lane);
+      if (lane == 0) slogit[w] = z;
     }
-  };
-  if (m < M)
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    float mx = -INFINITY, sum = 0.0f;
+    if (m < M)
 #pragma unroll 4
-    for (int i = w; i < parts; i += 32) {
-      const float2 v = part[static_cast<int64_t>(i) * M + m];
-      join(v.x, v.y);
+      for (int i = w; i < parts; i += 32) {
+        const float2 v = __ldcg(part + static_cast<int64_t>(i) * M + m);
+        ce_join(mx, sum, v.x, v.y);
+      }
+    smx[w][lane] = mx;
+    ssum[w][lane] = sum;
+    __syncthreads();
+    if (w == 0 && m < M) {
+      for (int i = 1; i < 32; ++i) ce_join(mx, sum, smx[i][lane], ssum[i][lane]);
+      const int64_t t = targets[m];
+      ce_finish(mx, sum, t >= 0 && t < V, slogit[lane], loss + m, lse + m);
     }
-  smx[w][r] = mx;
-  ssum[w][r] = sum;
-  __syncthreads();
-  if (w == 0 && m < M) {
-    for (int i = 1; i < 32; ++i) join(smx[i][r], ssum[i][r]);
+  } else {
+    __shared__ float smx[8], ssum[8];
+    const int64_t m = blockIdx.x;
     const int64_t t = targets[m];
-    if (t >= 0 && t < V) {
-      // mx, sum leave out the target: loss = log(1 + sum exp(mx - z))
-      const float z = slogit[r], d = mx - z;
-      float l;
-      if (mx == -INFINITY && sum == 0.0f)
-        l = z - z;  // no other entry with any weight (NaN for a non-finite z)
-      else
-        l = d <= 0.0f ? log1pf(sum * expf(d)) : d + logf(sum + expf(-d));
-      loss[m] = l;
-      lse[m] = z + l;
-    } else {
-      loss[m] = 0.0f;
-      lse[m] = mx + logf(sum);
+    const bool valid = t >= 0 && t < V;
+    float z = 0.0f;
+    if (w == 0 && valid) z = ce_target_dot(x + m * K, W + t * K, K, lane);
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    float mx = -INFINITY, sum = 0.0f;
+    for (int i = threadIdx.x; i < parts; i += 256) {
+      const float2 v = __ldcg(part + static_cast<int64_t>(i) * M + m);
+      ce_join(mx, sum, v.x, v.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)  // the lower lane's first, as in the wide cut
+      ce_join(mx, sum, __shfl_down_sync(0xFFFFFFFFu, mx, o),
+              __shfl_down_sync(0xFFFFFFFFu, sum, o));
+    if (lane == 0) {
+      smx[w] = mx;
+      ssum[w] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) ce_join(mx, sum, smx[i], ssum[i]);
+      ce_finish(mx, sum, valid, z, loss + m, lse + m);
     }
   }
 }

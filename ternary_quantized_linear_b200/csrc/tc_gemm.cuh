@@ -36,6 +36,11 @@
 // arrive, about 5 us; the epilogue warps take that pass on an empty tile
 // (`dry`) while the first copies and MMAs are under way.
 //
+// A product of fewer than 128 rows copies only those (rounded up to 8): the
+// MMA then takes whatever follows in the ring for the missing rows, whose sums
+// nobody reads, and the ring holds more stages.  Reading a head for one token
+// needs them: a 224 x 64 piece of it takes 3.6 us to arrive when all SMs ask.
+//
 // Every wait is bounded; on a timeout the kernel records the failure, lets
 // its copies land and exits.
 #pragma once
@@ -50,24 +55,23 @@ constexpr int kTgThreads = 384;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgKStep = 64;  // elements: one 128-byte swizzle row
 
-// Epi::kSlots blocks of Epi::kSlotBytes per epilogue warp for its tensors.
+constexpr int kTgMaxStages = 16;
+
+// Epi::kSlots blocks of Epi::kSlotBytes per epilogue warp for its tensors; the
+// rest of shared memory is the ring.
 template <int CG, int BN, class Epi>
 struct TgCfg {
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_ROWS = BN / CG;         // at most; bn / CG are used
-  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * 128;
   static constexpr int EPI_BYTES = kTgEpiWarps * Epi::kSlots * Epi::kSlotBytes;
-  static constexpr int FIT = (232448 - 2048 - EPI_BYTES) / STAGE_BYTES;
-  static constexpr int STAGES = FIT < 6 ? FIT : 6;
+  static constexpr int RING_BYTES = (232448 - 2048 - EPI_BYTES) / 1024 * 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;  // two accumulators
-  static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
+  static constexpr int OFF_EPI = RING_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   // full, empty, accfull[2], accempty[2], drain, parts, one per epilogue block
-  static constexpr int NBAR = 2 * STAGES + 6 + kTgEpiWarps * Epi::kSlots;
+  static constexpr int NBAR = 2 * kTgMaxStages + 6 + kTgEpiWarps * Epi::kSlots;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_DYN = OFF_MISC + 16 + 1024;
   static_assert(BN == 128 || BN == 256, "BN");
-  static_assert(STAGES >= 4, "ring");
+  static_assert(RING_BYTES >= 4 * (128 + BN / CG) * 128, "ring");
   static_assert(TMEM_COLS <= 512, "TMEM");
   static_assert(SMEM_DYN <= 232448, "shared memory");
 };
@@ -81,6 +85,8 @@ struct TgMaps {
 struct TgShape {
   int M, N;              // output rows and columns
   int bn;                // columns of a tile
+  int a_rows;            // rows of A that a stage holds (128, or fewer when M is smaller)
+  int stages, stage_bytes;
   int steps;             // 64-k steps of the contraction
   int mt, nt;            // tiles
   int per_batch;         // tiles of one batch entry
@@ -485,13 +491,13 @@ __global__ void __launch_bounds__(kTgThreads, 1)
 tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
                const typename Epi::Params ep) {
   using C = TgCfg<CG, BN, Epi>;
-  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::OFF_EPI >= 131072), "split");
+  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::RING_BYTES >= 131072), "split");
   extern __shared__ uint8_t tg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(tg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* accfull = empty + C::STAGES;
+  uint64_t* empty = full + kTgMaxStages;
+  uint64_t* accfull = empty + kTgMaxStages;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
   uint64_t* parts_bar = drain + 1;
@@ -506,10 +512,12 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   const int worker = static_cast<int>(blockIdx.x) / CLUSTER;
   const int workers = static_cast<int>(gridDim.x) / CLUSTER;
   const int b_rows = p.bn / CG;
-  const uint32_t stage_tx = static_cast<uint32_t>(CG * (C::A_BYTES + b_rows * 128));
+  const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * 128u;
+  const uint32_t stages = static_cast<uint32_t>(p.stages);
+  const uint32_t stage_tx = static_cast<uint32_t>(CG * p.stage_bytes);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -574,7 +582,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   }
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t it = 0;  // stages issued
+      uint32_t it = 0, s = 0, round = 0;  // stages issued, the ring's place
       bool ok = true;
       for (int t = worker; t < p.tiles && ok; t += workers) {
         const TgTile tile = tg_tile(p, t);
@@ -586,26 +594,29 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
           const CUtensorMap* ma = pass == 2 ? &maps.a_lo : &maps.a;
           const CUtensorMap* mb = pass == 1 ? &maps.b_lo : &maps.b;
           for (int j = k_lo; j < k_hi; ++j, ++it) {
-            const uint32_t s = it % C::STAGES, round = it / C::STAGES;
             if (round > 0 && !mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, limit)) {
               *abort_flag = 1;
               record_failure(p.status, DEV_TIMEOUT_PRODUCER);
               ok = false;
               break;
             }
-            const uint32_t dst = smem_u32(smem + s * C::STAGE_BYTES);
+            const uint32_t dst = smem_u32(smem) + s * static_cast<uint32_t>(p.stage_bytes);
             uint32_t bar = smem_u32(&full[s]);
             if (CG == 2) bar = map_to_rank(bar, 0);
             if (half_rank == 0) mbar_arrive_expect_tx(&full[s], stage_tx);
-            tg_load<CG>(ma, p.a_mn, 128, dst, a0, j * kTgKStep, tile.b, bar);
-            tg_load<CG>(mb, p.b_mn, b_rows, dst + C::A_BYTES, b0, j * kTgKStep, tile.b, bar);
+            tg_load<CG>(ma, p.a_mn, p.a_rows, dst, a0, j * kTgKStep, tile.b, bar);
+            tg_load<CG>(mb, p.b_mn, b_rows, dst + a_bytes, b0, j * kTgKStep, tile.b, bar);
+            if (++s == stages) {
+              s = 0;
+              ++round;
+            }
           }
         }
       }
       // The last commits must have arrived before this CTA's barriers go away.
-      const uint32_t from = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
+      const uint32_t from = it > stages ? it - stages : 0u;
       for (uint32_t i = from; i < it && ok; ++i)
-        if (!mbar_wait_bounded(&empty[i % C::STAGES], (i / C::STAGES) & 1u, abort_flag, limit)) {
+        if (!mbar_wait_bounded(&empty[i % stages], (i / stages) & 1u, abort_flag, limit)) {
           *abort_flag = 1;
           record_failure(p.status, DEV_TIMEOUT_PRODUCER);
           ok = false;
@@ -614,12 +625,12 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       // MMAs have consumed them all).
       if (*abort_flag && half_rank == 0)
         for (uint32_t i = from; i < it; ++i)
-          if (!mbar_wait_bounded(&full[i % C::STAGES], (i / C::STAGES) & 1u, nullptr, limit))
+          if (!mbar_wait_bounded(&full[i % stages], (i / stages) & 1u, nullptr, limit))
             record_failure(p.status, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
     if (lane == 0 && half_rank == 0) {
-      uint32_t it = 0;
+      uint32_t s = 0, ph = 0;
       int local = 0;
       bool ok = true;
       for (int t = worker; t < p.tiles && ok; t += workers, ++local) {
@@ -636,17 +647,16 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         }
         tc_fence_after_sync();
         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-        for (int j = 0; j < n_it; ++j, ++it) {
-          const uint32_t s = it % C::STAGES;
-          if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1u, abort_flag, limit)) {
+        for (int j = 0; j < n_it; ++j) {
+          if (!mbar_wait_bounded(&full[s], ph, abort_flag, limit)) {
             *abort_flag = 1;
             record_failure(p.status, DEV_TIMEOUT_MMA);
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a = smem_u32(smem + s * C::STAGE_BYTES);
-          const uint32_t b = a + C::A_BYTES;
+          const uint32_t a = smem_u32(smem) + s * static_cast<uint32_t>(p.stage_bytes);
+          const uint32_t b = a + a_bytes;
 #pragma unroll
           for (int kk = 0; kk < kTgKStep / 16; ++kk) {
             const uint64_t da = p.a_mn ? umma_desc_sw128_mnmajor(a + 2048 * kk)
@@ -656,6 +666,10 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
             tg_mma<CG>(d, da, db, p.idesc, (j > 0 || kk > 0) ? 1u : 0u);
           }
           tg_commit<CG>(&empty[s]);
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
         if (ok) tg_commit<CG>(&accfull[buf]);
       }
@@ -782,9 +796,11 @@ __device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensor
   if (st.lane == 0 && !t.dry) tma_store_3d(map, smem_u32(blk), col, t.row0, t.tile.b);
 }
 
-// D to bf16, times a device scalar when given.
+// D to bf16, times a device scalar when given.  Blocks of 32 x 64 (rows of 128
+// bytes, 128-byte swizzle): with rows of 64 bytes the copy engine wrote 2.6
+// TB/s, and a short contraction is all writing.
 struct TgStoreBf16 {
-  static constexpr int kSlots = 4, kSlotBytes = 2048;
+  static constexpr int kSlots = 2, kSlotBytes = 4096;
   struct Params {
     const float* scale;
   };
@@ -795,17 +811,22 @@ struct TgStoreBf16 {
   static __device__ __forceinline__ void run(const Params& e, const TgShape&, const TgMaps& m,
                                              const TgPart& t, TgStage& st, Src src) {
     const float f = e.scale && !t.dry ? __ldcg(e.scale) : 1.0f;
-    const int n = t.chunks();
+    // every other pair of chunks
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int c = t.first + i * t.step;
-      uint32_t r[32], w[16];
-      src.load(c, r);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * f, __uint_as_float(r[2 * j + 1]) * f);
+    for (int c = 2 * t.first; t.col0 + c < t.col_end; c += 128) {
       uint8_t* blk = tg_out_block<TgStoreBf16>(st);
-      block16_write(blk, st.lane, w);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[32], w[16];
+        src.load(c + 32 * h, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * f, __uint_as_float(r[2 * j + 1]) * f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(blk + block32_piece(st.lane, 4 * h + j)) =
+              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       tg_store_block(st, &m.out, blk, t.col0 + c, t);

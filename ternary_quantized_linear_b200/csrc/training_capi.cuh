@@ -31,6 +31,7 @@ struct TgTensor {
   const void* lo = nullptr;
   int64_t ld = 0, batch_stride = 0, batch = 1;
   CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  int block = 32;            // columns of a block: rows of 64 or 128 bytes
 };
 
 // How a product is cut: SM pairs on 256-row tiles (cg = 2) or single SMs on
@@ -80,16 +81,16 @@ bool make_operand_map(CUtensorMap* map, const TgOperand& o, const void* base, bo
                              tile_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// 32 x 32 blocks: rows of 64 bytes (16-bit) or 128 bytes (fp32).
+// Blocks of 32 rows, swizzled by their rows' 64 or 128 bytes.
 bool make_tensor_maps(CUtensorMap* map, CUtensorMap* map_lo, const TgTensor& t, int64_t M,
                       int64_t N) {
-  const CUtensorMapSwizzle swz = t.type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                     ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : CU_TENSOR_MAP_SWIZZLE_64B;
-  return (!t.p || make_tmap_3d(map, t.p, t.type, N, M, t.batch, t.ld, t.batch_stride, 32, 32,
+  const int row = t.block * (t.type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2);
+  const CUtensorMapSwizzle swz = row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                            : CU_TENSOR_MAP_SWIZZLE_64B;
+  return (!t.p || make_tmap_3d(map, t.p, t.type, N, M, t.batch, t.ld, t.batch_stride, t.block, 32,
                                swz)) &&
-         (!t.lo || make_tmap_3d(map_lo, t.lo, t.type, N, M, t.batch, t.ld, t.batch_stride, 32, 32,
-                                swz));
+         (!t.lo || make_tmap_3d(map_lo, t.lo, t.type, N, M, t.batch, t.ld, t.batch_stride,
+                                t.block, 32, swz));
 }
 
 int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) {
@@ -172,21 +173,28 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   const int workers = tg_workers<CG, BN, SPLIT, Epi>(ds.num_sms);
   if (workers < 1) return cuda_status(cudaErrorInvalidConfiguration);
   const int bn = g.plan.bn, b_rows = bn / CG;
+  // A K-major operand of fewer rows is copied as far as it goes.
+  const int a_rows = CG == 1 && !g.a.mn && g.M < 128 ? static_cast<int>(round_up(g.M, 8)) : 128;
   TgMaps maps;
   std::memset(&maps, 0, sizeof(maps));
-  if (!make_operand_map(&maps.a, g.a, g.a.p, g.bf16, g.M, g.Kc, g.batch, 128) ||
+  if (!make_operand_map(&maps.a, g.a, g.a.p, g.bf16, g.M, g.Kc, g.batch, a_rows) ||
       !make_operand_map(&maps.b, g.b, g.b.p, g.bf16, g.N, g.Kc, g.batch, b_rows) ||
       !make_tensor_maps(&maps.in, &maps.in_lo, g.in, g.M, g.N) ||
       !make_tensor_maps(&maps.out, &maps.out_lo, g.out, g.M, g.N))
     return BITNET_ERR_CUDA;
   if (g.passes == 3 &&
-      (!make_operand_map(&maps.a_lo, g.a, g.a.lo, g.bf16, g.M, g.Kc, g.batch, 128) ||
+      (!make_operand_map(&maps.a_lo, g.a, g.a.lo, g.bf16, g.M, g.Kc, g.batch, a_rows) ||
        !make_operand_map(&maps.b_lo, g.b, g.b.lo, g.bf16, g.N, g.Kc, g.batch, b_rows)))
     return BITNET_ERR_CUDA;
   TgShape p{};
   p.M = static_cast<int>(g.M);
   p.N = static_cast<int>(g.N);
   p.bn = bn;
+  p.a_rows = a_rows;
+  p.stage_bytes = (a_rows + b_rows) * 128;
+  // (the MMA reads 128 rows of A whatever was copied: within the ring)
+  p.stages = std::min({kTgMaxStages, C::RING_BYTES / p.stage_bytes,
+                       1 + (C::RING_BYTES - 16384) / p.stage_bytes});
   p.steps = static_cast<int>(ceil_div(g.Kc, kTgKStep));
   p.mt = static_cast<int>(ceil_div(g.M, 128 * CG));
   p.nt = static_cast<int>(ceil_div(g.N, bn));
@@ -538,8 +546,12 @@ BITNET_API bitnet_status bitnet_cross_entropy_forward(const void* x, const void*
   CeStats::Params ep{targets, reinterpret_cast<float2*>(ws + L.part)};
   st = launch_tg<256, CeStats>(*ds, g, ep, s);
   if (st != BITNET_OK) return st;
-  return launch_pdl(ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(M, 32))), 1024, s, ep.part,
-                    static_cast<int>(L.parts), static_cast<const __nv_bfloat16*>(x),
+  // (256 rows: a block per row is two waves of them, and the wide cut's
+  // neighbouring parts begin to count)
+  const bool wide = M > 256;
+  return launch_pdl(wide ? ce_join_kernel<true> : ce_join_kernel<false>,
+                    dim3(static_cast<unsigned>(wide ? ceil_div(M, 32) : M)), wide ? 1024 : 256, s,
+                    ep.part, static_cast<int>(L.parts), static_cast<const __nv_bfloat16*>(x),
                     static_cast<const __nv_bfloat16*>(W), targets, V, K, static_cast<int>(M),
                     loss, lse);
 }
@@ -660,6 +672,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.b.mn = true;
       g.out.p = static_cast<__nv_bfloat16*>(dW) + v0 * K;
       g.out.ld = K;
+      g.out.block = 64;
       g.M = cols;
       g.N = K;
       g.Kc = M;
