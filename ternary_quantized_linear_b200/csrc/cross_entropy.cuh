@@ -63,6 +63,7 @@ __device__ __forceinline__ float ce_target_dot(const __nv_bfloat16* __restrict__
 }
 
 struct CeStats {
+  static constexpr bool kAMn = false, kBMn = false, kBf16 = true;
   static constexpr int kSlots = 0, kSlotBytes = 0;
   struct Params {
     const int64_t* targets;
@@ -254,6 +255,7 @@ ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __res
 }
 
 struct CeGrad {
+  static constexpr bool kAMn = false, kBMn = false, kBf16 = true;
   static constexpr int kSlots = 2, kSlotBytes = 2048;
   struct Params {
     const int64_t* targets;

@@ -276,6 +276,7 @@ __device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const 
 // A = X X^T: its diagonal to D (fp32), the rest to R (fp16, and its low half
 // where the products take it).
 struct OrthoGram {
+  static constexpr bool kAMn = false, kBMn = false, kBf16 = false;
   static constexpr int kSlots = 2, kSlotBytes = 4096;
   struct Params {
     float* D;              // [batch][n]
@@ -312,6 +313,7 @@ struct OrthoGram {
 
 // R R, and from it Q (fp16) and a + E (fp32, the factor of X).
 struct OrthoPoly {
+  static constexpr bool kAMn = false, kBMn = false, kBf16 = false;
   static constexpr int kSlots = 3, kSlotBytes = 4096;
   struct Params {
     const float* D;
@@ -384,6 +386,7 @@ struct OrthoPoly {
 // X <- (a + E_i) X + Q X: the next X as two halves, or the result in bf16
 // (transposed back for a tall update).
 struct OrthoUpdate {
+  static constexpr bool kAMn = false, kBMn = true, kBf16 = false;
   static constexpr int kSlots = 3, kSlotBytes = 4096;
   struct Params {
     const float* E;

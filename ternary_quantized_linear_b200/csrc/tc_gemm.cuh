@@ -63,6 +63,8 @@ template <int CG, int BN, class Epi>
 struct TgCfg {
   static constexpr int EPI_BYTES = kTgEpiWarps * Epi::kSlots * Epi::kSlotBytes;
   static constexpr int RING_BYTES = (232448 - 2048 - EPI_BYTES) / 1024 * 1024;
+  static constexpr uint32_t PAIR_STAGES =
+      RING_BYTES / ((128 + BN / 2) * 128) < 6 ? RING_BYTES / ((128 + BN / 2) * 128) : 6;
   static constexpr uint32_t TMEM_COLS = 2 * BN;  // two accumulators
   static constexpr int OFF_EPI = RING_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
@@ -86,7 +88,7 @@ struct TgShape {
   int M, N;              // output rows and columns
   int bn;                // columns of a tile
   int a_rows;            // rows of A that a stage holds (128, or fewer when M is smaller)
-  int stages, stage_bytes;
+  int stages;            // of the ring (single SMs)
   int steps;             // 64-k steps of the contraction
   int mt, nt;            // tiles
   int per_batch;         // tiles of one batch entry
@@ -95,7 +97,6 @@ struct TgShape {
   int sym;               // only tiles with m >= n (square output)
   int group;             // m tiles that share one sweep over n
   int passes;
-  int a_mn, b_mn;
   uint32_t idesc;
   int* status;
   uint64_t wait_limit_ns;
@@ -279,10 +280,10 @@ __host__ __device__ constexpr uint32_t tg_idesc(int M, int N, bool bf16, bool a_
 }
 
 // One operand's part of a stage: `rows` rows from row0, 64 k from k0.
-template <int CG>
-__device__ __forceinline__ void tg_load(const CUtensorMap* map, bool mn, int rows, uint32_t dst,
-                                        int row0, int k0, int b, uint32_t bar) {
-  if (!mn) {
+template <int CG, bool MN>
+__device__ __forceinline__ void tg_load(const CUtensorMap* map, int rows, uint32_t dst, int row0,
+                                        int k0, int b, uint32_t bar) {
+  if constexpr (!MN) {
     tg_tma_load<CG>(dst, map, k0, row0, b, bar);
   } else {
     for (int i = 0; i < rows; i += 64)
@@ -483,7 +484,8 @@ __device__ __forceinline__ void dsmem_copy(uint32_t dst_cluster, uint32_t src, u
 
 // ------------------------------------------------------------------- kernel
 
-// Epi: struct with Params, kSlots, kSlotBytes, begin(...) (called before the
+// Epi: struct with Params, kAMn and kBMn (which operands are MN-major) and
+// kBf16 (else fp16), kSlots, kSlotBytes, begin(...) (called before the
 // accumulator is waited for), run(...), which takes the part's chunks, and
 // abandon(...) for a part that was begun and is not run.
 template <int CG, int BN, int SPLIT, class Epi>
@@ -511,13 +513,16 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   const uint64_t limit = p.wait_limit_ns;
   const int worker = static_cast<int>(blockIdx.x) / CLUSTER;
   const int workers = static_cast<int>(gridDim.x) / CLUSTER;
-  const int b_rows = p.bn / CG;
-  const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * 128u;
-  const uint32_t stages = static_cast<uint32_t>(p.stages);
-  const uint32_t stage_tx = static_cast<uint32_t>(CG * p.stage_bytes);
+  // Pairs always take whole 256 x 256 tiles.
+  const int a_rows = CG == 2 ? 128 : p.a_rows;
+  const int b_rows = CG == 2 ? BN / 2 : p.bn;
+  const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * 128u;
+  const uint32_t stage_bytes = static_cast<uint32_t>(a_rows + b_rows) * 128u;
+  const uint32_t stages = CG == 2 ? C::PAIR_STAGES : static_cast<uint32_t>(p.stages);
+  const uint32_t stage_tx = CG * stage_bytes;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -557,8 +562,8 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
     t.tile = tile;
     t.row0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank) + 32 * q;
     t.row = t.row0 + lane;
-    t.col0 = tile.n * p.bn;
-    t.col_end = min(p.N, t.col0 + p.bn);
+    t.col0 = tile.n * (CG == 2 ? BN : p.bn);
+    t.col_end = min(p.N, t.col0 + (CG == 2 ? BN : p.bn));
     t.first = 32 * half;
     t.step = 64;
     t.dry = false;
@@ -589,7 +594,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         int k_lo, k_hi;
         k_range(tile, k_lo, k_hi);
         const int a0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank);
-        const int b0 = tile.n * p.bn + b_rows * static_cast<int>(half_rank);
+        const int b0 = tile.n * (CG * b_rows) + b_rows * static_cast<int>(half_rank);
         for (int pass = 0; pass < p.passes && ok; ++pass) {
           const CUtensorMap* ma = pass == 2 ? &maps.a_lo : &maps.a;
           const CUtensorMap* mb = pass == 1 ? &maps.b_lo : &maps.b;
@@ -600,12 +605,12 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
               ok = false;
               break;
             }
-            const uint32_t dst = smem_u32(smem) + s * static_cast<uint32_t>(p.stage_bytes);
+            const uint32_t dst = smem_u32(smem) + s * stage_bytes;
             uint32_t bar = smem_u32(&full[s]);
             if (CG == 2) bar = map_to_rank(bar, 0);
             if (half_rank == 0) mbar_arrive_expect_tx(&full[s], stage_tx);
-            tg_load<CG>(ma, p.a_mn, p.a_rows, dst, a0, j * kTgKStep, tile.b, bar);
-            tg_load<CG>(mb, p.b_mn, b_rows, dst + a_bytes, b0, j * kTgKStep, tile.b, bar);
+            tg_load<CG, Epi::kAMn>(ma, a_rows, dst, a0, j * kTgKStep, tile.b, bar);
+            tg_load<CG, Epi::kBMn>(mb, b_rows, dst + a_bytes, b0, j * kTgKStep, tile.b, bar);
             if (++s == stages) {
               s = 0;
               ++round;
@@ -630,6 +635,15 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
     }
   } else if (warp == 1) {
     if (lane == 0 && half_rank == 0) {
+      // This one thread feeds the tensor cores of the pair, a step of 512
+      // cycles: whatever it need not compute per step is outside the loop or a
+      // constant (operand layouts as run-time choices cost 8 % of the rate).
+      const uint32_t a = smem_u32(smem);
+      const uint64_t desc_a = Epi::kAMn ? umma_desc_sw128_mnmajor(a) : umma_desc_sw128_kmajor(a);
+      const uint64_t desc_b = Epi::kBMn ? umma_desc_sw128_mnmajor(a + a_bytes)
+                                        : umma_desc_sw128_kmajor(a + a_bytes);
+      const uint32_t idesc =
+          CG == 2 ? tg_idesc(256, BN, Epi::kBf16, Epi::kAMn, Epi::kBMn) : p.idesc;
       uint32_t s = 0, ph = 0;
       int local = 0;
       bool ok = true;
@@ -655,16 +669,13 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a = smem_u32(smem) + s * static_cast<uint32_t>(p.stage_bytes);
-          const uint32_t b = a + a_bytes;
+          // (start addresses stay below 2^18: adding to the field is safe)
+          const uint64_t at = s * (stage_bytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kTgKStep / 16; ++kk) {
-            const uint64_t da = p.a_mn ? umma_desc_sw128_mnmajor(a + 2048 * kk)
-                                       : umma_desc_sw128_kmajor(a + 32 * kk);
-            const uint64_t db = p.b_mn ? umma_desc_sw128_mnmajor(b + 2048 * kk)
-                                       : umma_desc_sw128_kmajor(b + 32 * kk);
-            tg_mma<CG>(d, da, db, p.idesc, (j > 0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kTgKStep / 16; ++kk)
+            tg_mma<CG>(d, desc_a + at + (Epi::kAMn ? 128 : 2) * kk,
+                       desc_b + at + (Epi::kBMn ? 128 : 2) * kk, idesc,
+                       (kk > 0 || j > 0) ? 1u : 0u);
           tg_commit<CG>(&empty[s]);
           if (++s == stages) {
             s = 0;
@@ -797,9 +808,11 @@ __device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensor
 }
 
 // D to bf16, times a device scalar when given.  Blocks of 32 x 64 (rows of 128
-// bytes, 128-byte swizzle): with rows of 64 bytes the copy engine wrote 2.6
-// TB/s, and a short contraction is all writing.
+// bytes, 128-byte swizzle): a short contraction is all writing, and with rows
+// of 64 bytes the copy engine took 5 % longer for it (dW of 64 tokens over
+// 32000 x 2048 at 2.9 TB/s; a plain fill of that size reaches 3.5).
 struct TgStoreBf16 {
+  static constexpr bool kAMn = true, kBMn = true, kBf16 = true;
   static constexpr int kSlots = 2, kSlotBytes = 4096;
   struct Params {
     const float* scale;
@@ -838,6 +851,7 @@ struct TgStoreBf16 {
 // D (+ an fp32 tensor) to fp32, or times a device scalar to bf16; a slice of
 // a split contraction goes to its own [M][N] of the output.
 struct TgAccumulate {
+  static constexpr bool kAMn = false, kBMn = true, kBf16 = true;
   static constexpr int kSlots = 3, kSlotBytes = 4096;
   struct Params {
     int add;             // add `in`

@@ -17,12 +17,12 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 // ------------------------------------------------------------ matrix product
 
 // One operand: `rows` (m or n) x contraction, K-major (k contiguous) or
-// MN-major, row stride ld and batch stride in elements.
+// MN-major as the epilogue's product has it, row stride ld and batch stride in
+// elements.
 struct TgOperand {
   const void* p = nullptr;
   const void* lo = nullptr;
   int64_t ld = 0, batch_stride = 0;
-  bool mn = false;
 };
 
 // A tensor of the epilogue: [batch][M][N] with row stride ld.
@@ -45,7 +45,6 @@ struct TgProblem {
   TgOperand a, b;
   TgTensor in, out;
   int64_t M = 0, N = 0, Kc = 0, batch = 1;
-  bool bf16 = true;
   bool sym = false;
   int passes = 1;
   int ksplit = 1;            // slices of the contraction as tiles of their own
@@ -71,11 +70,11 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_operand_map(CUtensorMap* map, const TgOperand& o, const void* base, bool bf16,
+bool make_operand_map(CUtensorMap* map, const TgOperand& o, bool mn, const void* base, bool bf16,
                       int64_t rows, int64_t Kc, int64_t batch, int tile_rows) {
   const CUtensorMapDataType type =
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return o.mn ? make_tmap_3d(map, base, type, rows, Kc, batch, o.ld, o.batch_stride, 64, 64,
+  return mn ? make_tmap_3d(map, base, type, rows, Kc, batch, o.ld, o.batch_stride, 64, 64,
                              CU_TENSOR_MAP_SWIZZLE_128B)
               : make_tmap_3d(map, base, type, Kc, rows, batch, o.ld, o.batch_stride, 64,
                              tile_rows, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -174,27 +173,27 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   if (workers < 1) return cuda_status(cudaErrorInvalidConfiguration);
   const int bn = g.plan.bn, b_rows = bn / CG;
   // A K-major operand of fewer rows is copied as far as it goes.
-  const int a_rows = CG == 1 && !g.a.mn && g.M < 128 ? static_cast<int>(round_up(g.M, 8)) : 128;
+  const int a_rows = CG == 1 && !Epi::kAMn && g.M < 128 ? static_cast<int>(round_up(g.M, 8)) : 128;
   TgMaps maps;
   std::memset(&maps, 0, sizeof(maps));
-  if (!make_operand_map(&maps.a, g.a, g.a.p, g.bf16, g.M, g.Kc, g.batch, a_rows) ||
-      !make_operand_map(&maps.b, g.b, g.b.p, g.bf16, g.N, g.Kc, g.batch, b_rows) ||
+  if (!make_operand_map(&maps.a, g.a, Epi::kAMn, g.a.p, Epi::kBf16, g.M, g.Kc, g.batch, a_rows) ||
+      !make_operand_map(&maps.b, g.b, Epi::kBMn, g.b.p, Epi::kBf16, g.N, g.Kc, g.batch, b_rows) ||
       !make_tensor_maps(&maps.in, &maps.in_lo, g.in, g.M, g.N) ||
       !make_tensor_maps(&maps.out, &maps.out_lo, g.out, g.M, g.N))
     return BITNET_ERR_CUDA;
   if (g.passes == 3 &&
-      (!make_operand_map(&maps.a_lo, g.a, g.a.lo, g.bf16, g.M, g.Kc, g.batch, a_rows) ||
-       !make_operand_map(&maps.b_lo, g.b, g.b.lo, g.bf16, g.N, g.Kc, g.batch, b_rows)))
+      (!make_operand_map(&maps.a_lo, g.a, Epi::kAMn, g.a.lo, Epi::kBf16, g.M, g.Kc, g.batch, a_rows) ||
+       !make_operand_map(&maps.b_lo, g.b, Epi::kBMn, g.b.lo, Epi::kBf16, g.N, g.Kc, g.batch, b_rows)))
     return BITNET_ERR_CUDA;
   TgShape p{};
   p.M = static_cast<int>(g.M);
   p.N = static_cast<int>(g.N);
   p.bn = bn;
   p.a_rows = a_rows;
-  p.stage_bytes = (a_rows + b_rows) * 128;
   // (the MMA reads 128 rows of A whatever was copied: within the ring)
-  p.stages = std::min({kTgMaxStages, C::RING_BYTES / p.stage_bytes,
-                       1 + (C::RING_BYTES - 16384) / p.stage_bytes});
+  const int stage_bytes = (a_rows + b_rows) * 128;
+  p.stages = std::min({kTgMaxStages, C::RING_BYTES / stage_bytes,
+                       1 + (C::RING_BYTES - 16384) / stage_bytes});
   p.steps = static_cast<int>(ceil_div(g.Kc, kTgKStep));
   p.mt = static_cast<int>(ceil_div(g.M, 128 * CG));
   p.nt = static_cast<int>(ceil_div(g.N, bn));
@@ -209,9 +208,7 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   p.group = static_cast<int>(std::max<int64_t>(
       8, std::min<int64_t>(16, (32LL << 20) / (128LL * CG * 2 * g.Kc))));
   p.passes = g.passes;
-  p.a_mn = g.a.mn ? 1 : 0;
-  p.b_mn = g.b.mn ? 1 : 0;
-  p.idesc = tg_idesc(128 * CG, bn, g.bf16, g.a.mn, g.b.mn);
+  p.idesc = tg_idesc(128 * CG, bn, Epi::kBf16, Epi::kAMn, Epi::kBMn);
   p.status = ds.status;
   p.wait_limit_ns = kWaitLimitNs;
   cudaLaunchConfig_t cfg{};
@@ -621,7 +618,6 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.a.ld = L.cols;
       g.b.p = Wi;
       g.b.ld = K;
-      g.b.mn = true;
       g.M = M;
       g.N = K;
       g.Kc = cols;
@@ -666,10 +662,8 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       TgProblem g;
       g.a.p = gbuf;
       g.a.ld = L.cols;
-      g.a.mn = true;
       g.b.p = x;
       g.b.ld = K;
-      g.b.mn = true;
       g.out.p = static_cast<__nv_bfloat16*>(dW) + v0 * K;
       g.out.ld = K;
       g.out.block = 64;
@@ -767,7 +761,6 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     const double sr = fp16_scale(top[i] * top[i]), sq = fp16_scale(poly[i]);
     const double sy = fp16_scale(top[i + 1]);
     TgProblem g;
-    g.bf16 = false;
     g.batch = B;
     g.passes = passes;
     // A = X X^T
@@ -816,7 +809,6 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.b.lo = half_at(L.X_lo[from]);
     g.b.ld = L.ldx;
     g.b.batch_stride = xb;
-    g.b.mn = true;
     g.in.p = g.b.p;
     g.in.lo = g.b.lo;
     g.in.ld = L.ldx;
