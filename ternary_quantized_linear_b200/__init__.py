@@ -733,7 +733,8 @@ def _on(device, stream, run):
     handed to another stream's work."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            return run(ctypes.c_void_p(torch.cuda.current_stream(device.index).cuda_stream))
+            # (the current stream's pointer without building a Stream object)
+            return run(ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index)))
         with torch.cuda.device(device):
             return run(_stream())
     if stream.device != device:
@@ -783,8 +784,8 @@ def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=N
     dev = x.device
 
     def run(handle):
-        y = torch.empty((M,), dtype=torch.float32, device=dev) if loss is None else loss
-        z = torch.empty((M,), dtype=torch.float32, device=dev) if lse is None else lse
+        y = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
+        z = torch.empty(M, dtype=torch.float32, device=dev) if lse is None else lse
         ws = _scratch(workspace, nb, dev)
         _check("bitnet_cross_entropy_forward", lib.bitnet_cross_entropy_forward(
             _ptr(x), _ptr(W), _ptr(targets), M, V, K, _ptr(y), _ptr(z), _ptr(ws), ws.numel(),
@@ -818,9 +819,9 @@ def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_
     def run(handle):
         gx, gW = dx if need_dx else None, dW if need_dW else None
         if gx is None and need_dx:
-            gx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+            gx = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
         if gW is None and need_dW:
-            gW = torch.empty((V, K), dtype=torch.bfloat16, device=dev)
+            gW = torch.empty(V, K, dtype=torch.bfloat16, device=dev)
         ws = _scratch(workspace, nb, dev)
         _check("bitnet_cross_entropy_backward", lib.bitnet_cross_entropy_backward(
             _ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K, _ptr(gx), _ptr(gW),

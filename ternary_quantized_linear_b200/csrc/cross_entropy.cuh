@@ -70,7 +70,7 @@ struct CeStats {
     float2* part;          // [2 nt][M]: maximum, sum of exp(z - maximum)
   };
   static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
-                                               const TgPart&) {}
+                                               const TgShape&, const TgPart&) {}
   static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps&,
@@ -267,7 +267,7 @@ struct CeGrad {
     int64_t v0;            // first column of this piece
   };
   static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
-                                               const TgPart&) {}
+                                               const TgShape&, const TgPart&) {}
   static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape&, const TgMaps& m,

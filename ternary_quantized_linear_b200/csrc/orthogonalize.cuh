@@ -284,7 +284,7 @@ struct OrthoGram {
     float to_true, to_R;   // accumulator -> A, accumulator -> stored R
   };
   static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
-                                               const TgPart&) {}
+                                               const TgShape&, const TgPart&) {}
   static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
@@ -323,9 +323,14 @@ struct OrthoPoly {
     float acc_true, r_true, to_Q;
   };
   using In = TgInput<OrthoPoly>;
+  // D of this thread's row, and of the lane's column of the first chunk.
   static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
-                                               const TgPart& t) {
+                                               const TgShape& p, const TgPart& t) {
     In::begin(st, m, t, e.low != 0, 2048);
+    const float* D = e.D + static_cast<int64_t>(t.tile.b) * p.M;
+    st.pre[0] = t.live ? __ldcg(D + t.row) : 0.0f;
+    const int col = t.col0 + t.first + st.lane;
+    st.pre[1] = col < p.N ? __ldcg(D + col) : 0.0f;
   }
   static __device__ __forceinline__ void abandon(TgStage& st, const Params&, const TgPart& t) {
     In::abandon(st, t);
@@ -335,12 +340,14 @@ struct OrthoPoly {
                                              const TgPart& t, TgStage& st, Src src) {
     const bool mirror = p.sym && t.tile.m != t.tile.n, low = e.low != 0;
     const float* D = e.D + static_cast<int64_t>(t.tile.b) * p.M;
-    const float di = t.live ? __ldcg(D + t.row) : 0.0f;
+    const float di = st.pre[0];
+    float dl_next = st.pre[1];
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
       const int c = t.first + k * t.step, col = t.col0 + c;
-      const float dl = !t.dry && col + st.lane < p.N ? __ldcg(D + col + st.lane) : 0.0f;
+      const float dl = dl_next;
+      if (k + 1 < n && col + t.step + st.lane < p.N) dl_next = __ldcg(D + col + t.step + st.lane);
       uint8_t* blk = st.base + (st.seq % kSlots) * kSlotBytes;
       if (!In::wait(st, t, k)) break;
       uint32_t r[32], w[16];
@@ -396,9 +403,10 @@ struct OrthoUpdate {
     float acc_true, x_true, to_Y;
   };
   using In = TgInput<OrthoUpdate>;
-  static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params&,
-                                               const TgPart& t) {
+  static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
+                                               const TgShape& p, const TgPart& t) {
     In::begin(st, m, t, true, 2048);
+    st.pre[0] = t.live ? __ldcg(e.E + static_cast<int64_t>(t.tile.b) * p.M + t.row) : 0.0f;
   }
   static __device__ __forceinline__ void abandon(TgStage& st, const Params&, const TgPart& t) {
     In::abandon(st, t);
@@ -406,8 +414,7 @@ struct OrthoUpdate {
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
                                              const TgPart& t, TgStage& st, Src src) {
-    const float ei =
-        t.live ? __ldcg(e.E + static_cast<int64_t>(t.tile.b) * p.M + t.row) * e.x_true : 0.0f;
+    const float ei = st.pre[0] * e.x_true;
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {

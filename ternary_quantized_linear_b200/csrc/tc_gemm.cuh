@@ -344,6 +344,7 @@ struct TgStage {
   volatile int* abort_flag;
   int* status;
   uint64_t limit;
+  float pre[2];         // values that begin() loads ahead for run()
 };
 
 __device__ __forceinline__ uint32_t block16_piece(int lane, int j) {
@@ -579,20 +580,22 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   st.abort_flag = abort_flag;
   st.status = p.status;
   st.limit = limit;
+  st.pre[0] = st.pre[1] = 0.0f;
   const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
 
-  if (warp < 4) {
-    pdl_wait_prior_grid();
-    pdl_launch_dependents();
-  }
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0, s = 0, round = 0;  // stages issued, the ring's place
       bool ok = true;
-      for (int t = worker; t < p.tiles && ok; t += workers) {
-        const TgTile tile = tg_tile(p, t);
-        int k_lo, k_hi;
-        k_range(tile, k_lo, k_hi);
+      // The first tile's place is worked out before the launch before has
+      // ended (its divisions take 1500 cycles with cold instructions).
+      int t = worker;
+      TgTile tile = tg_tile(p, t);
+      int k_lo, k_hi;
+      k_range(tile, k_lo, k_hi);
+      pdl_wait_prior_grid();
+      pdl_launch_dependents();
+      while (true) {
         const int a0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank);
         const int b0 = tile.n * (CG * b_rows) + b_rows * static_cast<int>(half_rank);
         for (int pass = 0; pass < p.passes && ok; ++pass) {
@@ -617,6 +620,10 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
             }
           }
         }
+        t += workers;
+        if (t >= p.tiles || !ok) break;
+        tile = tg_tile(p, t);
+        k_range(tile, k_lo, k_hi);
       }
       // The last commits must have arrived before this CTA's barriers go away.
       const uint32_t from = it > stages ? it - stages : 0u;
@@ -705,12 +712,12 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       }
       st.seq = 0;
     }
+    TgPart part = part_of(tg_tile(p, worker), q, half);
     pdl_wait_prior_grid();
     int local = 0;
-    for (int t = worker; t < p.tiles; t += workers, ++local) {
+    for (int t = worker; t < p.tiles; ++local) {
       const int buf = local & 1;
-      const TgPart part = part_of(tg_tile(p, t), q, half);
-      if constexpr (SPLIT == 1) Epi::begin(st, maps, ep, part);
+      if constexpr (SPLIT == 1) Epi::begin(st, maps, ep, p, part);
       const bool ok = __all_sync(
           0xFFFFFFFFu, mbar_wait_bounded(&accfull[buf], static_cast<uint32_t>(local >> 1) & 1u,
                                          abort_flag, limit));
@@ -744,6 +751,8 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         else
           mbar_arrive(&accempty[buf]);
       }
+      t += workers;
+      if (t < p.tiles) part = part_of(tg_tile(p, t), q, half);
     }
   }
   __syncwarp();
@@ -770,7 +779,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       part.first = 32 * (static_cast<int>(rank) * kChunks + half);
       part.step = 1 << 20;
       const bool run = *abort_flag == 0;
-      if (run) Epi::begin(st, maps, ep, part);
+      if (run) Epi::begin(st, maps, ep, p, part);
       const bool ok = __all_sync(0xFFFFFFFFu,
                                  mbar_wait_bounded(parts_bar, 0u, nullptr, limit));
       if (!ok && lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
@@ -818,7 +827,7 @@ struct TgStoreBf16 {
     const float* scale;
   };
   static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
-                                               const TgPart&) {}
+                                               const TgShape&, const TgPart&) {}
   static __device__ __forceinline__ void abandon(TgStage&, const Params&, const TgPart&) {}
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape&, const TgMaps& m,
@@ -860,7 +869,7 @@ struct TgAccumulate {
   };
   using In = TgInput<TgAccumulate>;
   static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
-                                               const TgPart& t) {
+                                               const TgShape&, const TgPart& t) {
     if (e.add)
       In::begin(st, m, t, false, 4096);
     else if (st.lane == 0)

@@ -165,16 +165,26 @@ int tg_workers(int num_sms) {
   return workers[dev];
 }
 
+// A product ready to launch: its tensor maps and shape (a step that comes
+// again with the same tensors reuses them; encoding the six maps of one
+// product takes the host as long as half a launch).
+struct TgReady {
+  bool done = false;
+  TgMaps maps;
+  TgShape shape;
+  int workers = 0;
+};
+
 template <int CG, int BN, int SPLIT, class Epi>
-bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
-                            const typename Epi::Params& ep, cudaStream_t stream) {
+bitnet_status prepare_tg(const DeviceState& ds, const TgProblem& g, TgReady& r) {
   using C = TgCfg<CG, BN, Epi>;
-  const int workers = tg_workers<CG, BN, SPLIT, Epi>(ds.num_sms);
-  if (workers < 1) return cuda_status(cudaErrorInvalidConfiguration);
+  r.workers = tg_workers<CG, BN, SPLIT, Epi>(ds.num_sms);
+  if (r.workers < 1) return cuda_status(cudaErrorInvalidConfiguration);
   const int bn = g.plan.bn, b_rows = bn / CG;
   // A K-major operand of fewer rows is copied as far as it goes.
-  const int a_rows = CG == 1 && !Epi::kAMn && g.M < 128 ? static_cast<int>(round_up(g.M, 8)) : 128;
-  TgMaps maps;
+  const int a_rows =
+      CG == 1 && !Epi::kAMn && g.M < 128 ? static_cast<int>(round_up(g.M, 8)) : 128;
+  TgMaps& maps = r.maps;
   std::memset(&maps, 0, sizeof(maps));
   if (!make_operand_map(&maps.a, g.a, Epi::kAMn, g.a.p, Epi::kBf16, g.M, g.Kc, g.batch, a_rows) ||
       !make_operand_map(&maps.b, g.b, Epi::kBMn, g.b.p, Epi::kBf16, g.N, g.Kc, g.batch, b_rows) ||
@@ -182,10 +192,13 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
       !make_tensor_maps(&maps.out, &maps.out_lo, g.out, g.M, g.N))
     return BITNET_ERR_CUDA;
   if (g.passes == 3 &&
-      (!make_operand_map(&maps.a_lo, g.a, Epi::kAMn, g.a.lo, Epi::kBf16, g.M, g.Kc, g.batch, a_rows) ||
-       !make_operand_map(&maps.b_lo, g.b, Epi::kBMn, g.b.lo, Epi::kBf16, g.N, g.Kc, g.batch, b_rows)))
+      (!make_operand_map(&maps.a_lo, g.a, Epi::kAMn, g.a.lo, Epi::kBf16, g.M, g.Kc, g.batch,
+                         a_rows) ||
+       !make_operand_map(&maps.b_lo, g.b, Epi::kBMn, g.b.lo, Epi::kBf16, g.N, g.Kc, g.batch,
+                         b_rows)))
     return BITNET_ERR_CUDA;
-  TgShape p{};
+  TgShape& p = r.shape;
+  p = TgShape{};
   p.M = static_cast<int>(g.M);
   p.N = static_cast<int>(g.N);
   p.bn = bn;
@@ -211,9 +224,23 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   p.idesc = tg_idesc(128 * CG, bn, Epi::kBf16, Epi::kAMn, Epi::kBMn);
   p.status = ds.status;
   p.wait_limit_ns = kWaitLimitNs;
+  r.done = true;
+  return BITNET_OK;
+}
+
+template <int CG, int BN, int SPLIT, class Epi>
+bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
+                            const typename Epi::Params& ep, cudaStream_t stream, TgReady* ready) {
+  using C = TgCfg<CG, BN, Epi>;
+  TgReady own;
+  TgReady& r = ready ? *ready : own;
+  if (!r.done) {
+    const bitnet_status st = prepare_tg<CG, BN, SPLIT, Epi>(ds, g, r);
+    if (st != BITNET_OK) return st;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(
-      CG * SPLIT * (SPLIT > 1 ? p.tiles : std::min(workers, p.tiles))));
+      CG * SPLIT * (SPLIT > 1 ? r.shape.tiles : std::min(r.workers, r.shape.tiles))));
   cfg.blockDim = dim3(kTgThreads);
   cfg.dynamicSmemBytes = C::SMEM_DYN;
   cfg.stream = stream;
@@ -226,25 +253,28 @@ bitnet_status launch_tg_cfg(const DeviceState& ds, const TgProblem& g,
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG * SPLIT > 1 ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, tc_gemm_kernel<CG, BN, SPLIT, Epi>, maps, p, ep));
+  return cuda_status(
+      cudaLaunchKernelEx(&cfg, tc_gemm_kernel<CG, BN, SPLIT, Epi>, r.maps, r.shape, ep));
 }
 
 // Pairs of 256 columns, or single SMs with tiles of up to BN1.
 template <int BN1, class Epi>
 bitnet_status launch_tg(const DeviceState& ds, const TgProblem& g,
-                        const typename Epi::Params& ep, cudaStream_t stream) {
-  return g.plan.cg == 2 ? launch_tg_cfg<2, 256, 1, Epi>(ds, g, ep, stream)
-                        : launch_tg_cfg<1, BN1, 1, Epi>(ds, g, ep, stream);
+                        const typename Epi::Params& ep, cudaStream_t stream,
+                        TgReady* ready = nullptr) {
+  return g.plan.cg == 2 ? launch_tg_cfg<2, 256, 1, Epi>(ds, g, ep, stream, ready)
+                        : launch_tg_cfg<1, BN1, 1, Epi>(ds, g, ep, stream, ready);
 }
 
 // The same with the contraction of a 128 x 128 tile shared by a cluster.
 template <class Epi>
 bitnet_status launch_tg_split(const DeviceState& ds, const TgProblem& g,
-                              const typename Epi::Params& ep, cudaStream_t stream) {
+                              const typename Epi::Params& ep, cudaStream_t stream,
+                              TgReady* ready) {
   switch (g.plan.split) {
-    case 2: return launch_tg_cfg<1, 128, 2, Epi>(ds, g, ep, stream);
-    case 4: return launch_tg_cfg<1, 128, 4, Epi>(ds, g, ep, stream);
-    default: return launch_tg<128, Epi>(ds, g, ep, stream);
+    case 2: return launch_tg_cfg<1, 128, 2, Epi>(ds, g, ep, stream, ready);
+    case 4: return launch_tg_cfg<1, 128, 4, Epi>(ds, g, ep, stream, ready);
+    default: return launch_tg<128, Epi>(ds, g, ep, stream, ready);
   }
 }
 
@@ -755,6 +785,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
   const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes, 4);
   // The result goes out by TMA where its rows are whole 16-byte pieces.
   const bool direct = !tall && L.k % 8 != 0;
+  TgReady gram_ready[2], poly_ready, update_ready[2], last_ready;
   for (int i = 0; i < steps; ++i) {
     const double* c = coefficients + 3 * i;
     const int from = i & 1, to = from ^ 1;
@@ -781,7 +812,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.plan = gram_plan;
     OrthoGram::Params gram{D, L.split ? 1 : 0, static_cast<float>(1.0 / (sx * sx)),
                            static_cast<float>(sr / (sx * sx))};
-    st = launch_tg_split<OrthoGram>(*ds, g, gram, s);
+    st = launch_tg_split<OrthoGram>(*ds, g, gram, s, &gram_ready[from]);
     if (st != BITNET_OK) return st;
     // R R -> Q, E
     g.Kc = L.n;
@@ -798,7 +829,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
                              static_cast<float>(c[1]), static_cast<float>(c[2]),
                              static_cast<float>(1.0 / (sr * sr)), static_cast<float>(1.0 / sr),
                              static_cast<float>(sq)};
-    st = launch_tg_split<OrthoPoly>(*ds, g, poly_p, s);
+    st = launch_tg_split<OrthoPoly>(*ds, g, poly_p, s, &poly_ready);
     if (st != BITNET_OK) return st;
     // X <- E X + Q X
     g.sym = false;
@@ -830,7 +861,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     OrthoUpdate::Params up{E, last ? static_cast<__nv_bfloat16*>(O) : nullptr, tall ? 1 : 0,
                            direct ? 1 : 0, static_cast<float>(1.0 / (sq * sx)),
                            static_cast<float>(1.0 / sx), static_cast<float>(sy)};
-    st = launch_tg_split<OrthoUpdate>(*ds, g, up, s);
+    st = launch_tg_split<OrthoUpdate>(*ds, g, up, s, last ? &last_ready : &update_ready[from]);
     if (st != BITNET_OK) return st;
     sx = sy;
   }
