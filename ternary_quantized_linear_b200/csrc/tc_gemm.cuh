@@ -552,9 +552,9 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
 
-  // Contraction steps of a tile that this CTA (or pair) takes.
-  auto k_range = [&](const TgTile& tile, int& lo, int& hi) {
-    const int slice = SPLIT > 1 ? static_cast<int>(rank) : tile.split;
+  // Contraction steps of a tile's slice that this CTA (or pair) takes.
+  auto k_range = [&](int split, int& lo, int& hi) {
+    const int slice = SPLIT > 1 ? static_cast<int>(rank) : split;
     lo = slice * p.split_steps;
     hi = min(p.steps, lo + p.split_steps);
   };
@@ -592,7 +592,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       int t = worker;
       TgTile tile = tg_tile(p, t);
       int k_lo, k_hi;
-      k_range(tile, k_lo, k_hi);
+      k_range(tile.split, k_lo, k_hi);
       pdl_wait_prior_grid();
       pdl_launch_dependents();
       while (true) {
@@ -623,7 +623,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         t += workers;
         if (t >= p.tiles || !ok) break;
         tile = tg_tile(p, t);
-        k_range(tile, k_lo, k_hi);
+        k_range(tile.split, k_lo, k_hi);
       }
       // The last commits must have arrived before this CTA's barriers go away.
       const uint32_t from = it > stages ? it - stages : 0u;
@@ -657,7 +657,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       for (int t = worker; t < p.tiles && ok; t += workers, ++local) {
         const int buf = local & 1;
         int k_lo, k_hi;
-        k_range(tg_tile(p, t), k_lo, k_hi);
+        k_range(p.ksplit > 1 ? t % p.ksplit : 0, k_lo, k_hi);
         const int n_it = (k_hi - k_lo) * p.passes;
         if (local >= 2 && !mbar_wait_bounded(&accempty[buf],
                                              static_cast<uint32_t>((local >> 1) - 1) & 1u,
