@@ -496,10 +496,12 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
  * Shapes: K % 8 == 0, 8 <= K <= BITNET_MAX_K, 1 <= V <= BITNET_MAX_N,
  * M <= BITNET_MAX_M, ceil(M/128) * ceil(V/128) <= 2^30; else
  * BITNET_ERR_UNSUPPORTED_SHAPE (and a workspace size of 0).
- * x, W, dx, dW 16-byte aligned, targets 8, the rest 4; workspace >= the size
- * query, 256-byte aligned, contents on entry irrelevant; one per call in
- * flight.  The backward takes lse as the forward wrote it.
- * The same inputs give the same bits on every call.
+ * x, W, dx, dW 16-byte aligned, targets 8, the rest 4; outputs must not
+ * overlap inputs; workspace >= the size query, 256-byte aligned, contents on
+ * entry irrelevant; one per call in flight.  The backward takes lse as the
+ * forward wrote it.  The same inputs give the same bits on every call.
+ * Make the first call on a device before any stream capture there (it looks
+ * up the kernels' resources); later ones may be captured.
  * ---------------------------------------------------------------------- */
 BITNET_API size_t bitnet_cross_entropy_forward_workspace_bytes(int64_t M, int64_t V, int64_t K);
 BITNET_API bitnet_status bitnet_cross_entropy_forward(const void *x, const void *W,
@@ -536,7 +538,8 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void *x, const void
  * 128 x 128 in all.  U, O 16-byte aligned; workspace >= the size query (0,
  * and NULL allowed, for updates of up to 128 x 2048 or 2048 x 128), 256-byte
  * aligned, contents on entry irrelevant; one per call in flight.
- * The same input gives the same bits on every call.
+ * The same input gives the same bits on every call.  As above, the first call
+ * on a device comes before any stream capture there.
  * ---------------------------------------------------------------------- */
 BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K);
 BITNET_API bitnet_status bitnet_orthogonalize(const void *U, int u_dtype, int64_t B, int64_t N,

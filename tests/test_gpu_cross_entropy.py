@@ -82,7 +82,7 @@ def _run(x, W, t, d):
 SHAPES = [(1, 1, 8), (1, 2, 8), (1, 100, 64), (1, 5003, 520), (3, 31, 72), (5, 257, 64),
           (16, 40000, 64), (17, 33, 8), (64, 1000, 264), (127, 300, 64), (128, 256, 128),
           (129, 255, 136), (130, 3000, 72), (300, 5003, 520), (513, 999, 1000), (1025, 2049, 64),
-          (2000, 700, 256)]
+          (2000, 700, 256), (4500, 1500, 64)]
 
 
 @pytest.mark.parametrize("M,V,K", SHAPES)
@@ -98,6 +98,14 @@ def test_vocabulary_in_pieces():
     M, V, K = 3000, 50000, 72
     x, W, t, d = _inputs(M, V, K, seed=5)
     t[-1], t[-3] = V - 1, 0
+    exact, tol = _exact(x, W, t, d)
+    _check(_run(x, W, t, d), exact, tol)
+
+
+def test_vocabulary_in_pieces_without_slices():
+    # dx has tiles enough for every SM: its pieces meet in the fp32 sum itself
+    M, V, K = 5000, 27000, 2048
+    x, W, t, d = _inputs(M, V, K, seed=6, sigma=0.02)
     exact, tol = _exact(x, W, t, d)
     _check(_run(x, W, t, d), exact, tol)
 

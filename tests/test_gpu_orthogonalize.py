@@ -79,7 +79,7 @@ def _check(U, got, rows=None, eps=1e-7):
 SHAPES = [(1, 1), (1, 7), (9, 1), (8, 8), (3, 300), (64, 64), (65, 63), (128, 128), (128, 129),
           (127, 257), (100, 640), (128, 2048), (2048, 128), (2047, 33), (128, 2049), (2056, 72),
           (129, 129), (192, 200), (193, 193), (200, 1001), (256, 256), (257, 300), (300, 257),
-          (512, 1024), (1024, 513), (777, 2731)]
+          (512, 1024), (1024, 513), (777, 2731), (1100, 1153), (1300, 1280), (2400, 2500)]
 
 
 @pytest.mark.parametrize("kind", ["flat", "lowrank"])
@@ -131,6 +131,24 @@ def test_zero_and_non_finite(N, K):
     got = tql.bitnet_orthogonalize(U)
     assert torch.isnan(got[1]).all()
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    U[1, 3, 4] = float("inf")
+    got = tql.bitnet_orthogonalize(U)
+    assert torch.isnan(got[1]).all() and torch.equal(got[0], want[0])
+
+
+def test_strided_and_misaligned_updates_are_refused():
+    U = _update(1, 40, 64, "flat")[0]
+    with pytest.raises(ValueError):
+        tql.bitnet_orthogonalize(U.T)
+    flat = torch.zeros(40 * 64 + 1, device="cuda")
+    with pytest.raises(tql.BitnetError) as e:
+        tql.bitnet_orthogonalize(flat[1:].view(40, 64))
+    assert e.value.code == tql.BITNET_ERR_MISALIGNED
+    empty = tql.bitnet_orthogonalize(torch.zeros(0, 40, 64, device="cuda"))
+    assert empty.shape == (0, 40, 64)
+    with pytest.raises(tql.BitnetError) as e:
+        tql.bitnet_orthogonalize(torch.zeros(3, 0, device="cuda"))
+    assert e.value.code == tql.BITNET_ERR_UNSUPPORTED_SHAPE
 
 
 @pytest.mark.parametrize("N,K", [(40, 100), (260, 300)])
