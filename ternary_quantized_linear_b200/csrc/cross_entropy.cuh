@@ -321,12 +321,13 @@ ce_join_dx_kernel(const float* __restrict__ part, int slices, int64_t stride,
                   const float* __restrict__ scale, __nv_bfloat16* __restrict__ out) {
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const float f = *scale;
+  const float f = __ldcg(scale);
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n4;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    float4 s = add ? reinterpret_cast<const float4*>(add)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = add ? __ldcg(reinterpret_cast<const float4*>(add) + i)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < slices; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(part + k * stride + 4 * i);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part + k * stride) + i);
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;

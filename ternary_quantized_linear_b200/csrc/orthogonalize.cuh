@@ -245,7 +245,7 @@ __device__ __forceinline__ void ortho_pack_rest(const float (&v)[32], const uint
 // element (r, j) of the chunk goes to piece r / 8 of row j there.
 __device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const TgPart& t,
                                             uint8_t* blk, int col, const float (&v)[32],
-                                            bool low, bool mirror, int rows) {
+                                            bool low, bool mirror) {
   uint32_t w[16];
   ortho_pack(v, w);
   block16_write(blk, st.lane, w);
@@ -263,11 +263,11 @@ __device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const 
   }
   fence_proxy_async_smem();
   __syncwarp();
-  if (st.lane == 0 && !t.dry) {
+  if (st.lane == 0 && t.any) {
     tma_store_3d(&m.out, smem_u32(blk), col, t.row0, t.tile.b);
     if (low)
       tma_store_3d(&m.out_lo, smem_u32(blk + 2048), col, t.row0, t.tile.b);
-    else if (mirror && t.row0 < rows)
+    else if (mirror)
       tma_store_3d(&m.out, smem_u32(blk + 2048), t.row0, col, t.tile.b);
   }
   if (st.lane == 0) bulk_commit();
@@ -306,7 +306,7 @@ struct OrthoGram {
       }
       if (t.live && at >= 0 && at < 32)
         e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.to_true;
-      ortho_store(st, m, t, tg_out_block<OrthoGram>(st), col, v, e.low != 0, mirror, p.M);
+      ortho_store(st, m, t, tg_out_block<OrthoGram>(st), col, v, e.low != 0, mirror);
     }
   }
 };
@@ -384,7 +384,7 @@ struct OrthoPoly {
         e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
             e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr_ii), e.b * di);
       __syncwarp();  // the whole block was read
-      ortho_store(st, m, t, blk, col, v, low, mirror, p.M);
+      ortho_store(st, m, t, blk, col, v, low, mirror);
       In::next(st, m, t, k, low, 2048);
     }
   }
@@ -445,7 +445,7 @@ struct OrthoUpdate {
       if (!e.out) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= e.to_Y;
-        ortho_store(st, m, t, blk, col, v, true, false, p.M);
+        ortho_store(st, m, t, blk, col, v, true, false);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);

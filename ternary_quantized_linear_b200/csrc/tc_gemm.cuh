@@ -324,6 +324,7 @@ struct TgPart {
   int first, step;      // the warp's chunks: columns col0 + first + i * step, 32 each
   bool dry;             // an empty pass: no tensor is read or written
   bool live;            // this thread's row exists (never in a dry pass)
+  bool any;             // the warp's first row does: there is something to store
 
   __device__ __forceinline__ int chunks() const {
     const int w = col_end - col0 - first;
@@ -569,6 +570,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
     t.step = 64;
     t.dry = false;
     t.live = t.row < p.M;
+    t.any = t.row0 < p.M;
     return t;
   };
   const int q = warp & 3, half = (warp - 4) >> 2;
@@ -701,7 +703,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
     {
       TgPart t = part_of(TgTile{0, 0, 0, 0}, q, half);
       t.dry = true;
-      t.live = false;
+      t.live = t.any = false;
       t.first = 0;
       t.col_end = min(t.col_end, 32);
       if constexpr (SPLIT == 1) {
@@ -813,7 +815,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 // Store a chunk's block and count it as one group of this warp.
 __device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensorMap* map,
                                                const uint8_t* blk, int col, const TgPart& t) {
-  if (st.lane == 0 && !t.dry) tma_store_3d(map, smem_u32(blk), col, t.row0, t.tile.b);
+  if (st.lane == 0 && t.any) tma_store_3d(map, smem_u32(blk), col, t.row0, t.tile.b);
 }
 
 // D to bf16, times a device scalar when given.  Blocks of 32 x 64 (rows of 128
