@@ -217,6 +217,14 @@ __device__ __forceinline__ void ortho_store_mirror(uint16_t* base, int64_t ld, i
           static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
 }
 
+// Entry `at` (0..31) of a chunk's accumulators, by selects.
+__device__ __forceinline__ float chunk_pick(const uint32_t (&r)[32], int at) {
+  uint32_t v = 0u;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v = i == at ? r[i] : v;
+  return __uint_as_float(v);
+}
+
 __device__ __forceinline__ void ortho_pack(const float (&v)[32], uint32_t (&hi)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -296,16 +304,17 @@ struct OrthoGram {
       const int c = t.first + k * t.step, col = t.col0 + c;
       uint32_t r[32];
       src.load(c, r);
-      float v[32], d = 0.0f;
-      const int at = t.row - col;  // the diagonal's place in the chunk
+      float v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float z = __uint_as_float(r[i]);
-        if (i == at) d = z;
-        v[i] = i == at ? 0.0f : z * e.to_R;
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * e.to_R;
+      if (t.row0 < col + 32 && col < t.row0 + 32) {  // the diagonal passes this chunk
+        const int at = t.row - col;
+        const float d = chunk_pick(r, at);
+        if (t.live && at >= 0 && at < 32)
+          e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.to_true;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i == at ? 0.0f : v[i];
       }
-      if (t.live && at >= 0 && at < 32)
-        e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.to_true;
       ortho_store(st, m, t, tg_out_block<OrthoGram>(st), col, v, e.low != 0, mirror);
     }
   }
@@ -342,6 +351,10 @@ struct OrthoPoly {
     const float* D = e.D + static_cast<int64_t>(t.tile.b) * p.M;
     const float di = st.pre[0];
     float dl_next = st.pre[1];
+    // to_Q (c R R + (b + c (D_i + D_j)) R), from the accumulator and stored R
+    const float kr = e.c * e.acc_true * e.to_Q;
+    const float kd = e.c * e.r_true * e.to_Q;
+    const float ki = __fmaf_rn(e.c, di, e.b) * e.r_true * e.to_Q;
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
@@ -369,20 +382,20 @@ struct OrthoPoly {
         }
       }
       src.load(c, r);
-      const int at = t.row - col;  // the diagonal's place in the chunk
-      float rr_ii = 0.0f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float rr = __uint_as_float(r[i]) * e.acc_true;
-        const float x = v[i] * e.r_true;
         const float dj = __shfl_sync(0xFFFFFFFFu, dl, i);
-        if (i == at) rr_ii = rr;
-        v[i] = i == at ? 0.0f
-                       : __fmaf_rn(e.c, __fmaf_rn(di + dj, x, rr), e.b * x) * e.to_Q;
+        v[i] = __fmaf_rn(__fmaf_rn(kd, dj, ki), v[i], __uint_as_float(r[i]) * kr);
       }
-      if (t.live && at >= 0 && at < 32)
-        e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
-            e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr_ii), e.b * di);
+      if (t.row0 < col + 32 && col < t.row0 + 32) {  // the diagonal passes this chunk
+        const int at = t.row - col;
+        const float rr = chunk_pick(r, at) * e.acc_true;
+        if (t.live && at >= 0 && at < 32)
+          e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
+              e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr), e.b * di);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i == at ? 0.0f : v[i];
+      }
       __syncwarp();  // the whole block was read
       ortho_store(st, m, t, blk, col, v, low, mirror);
       In::next(st, m, t, k, low, 2048);
@@ -414,37 +427,28 @@ struct OrthoUpdate {
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
                                              const TgPart& t, TgStage& st, Src src) {
-    const float ei = st.pre[0] * e.x_true;
+    const float to = e.out ? 1.0f : e.to_Y;
+    const float ei = st.pre[0] * e.x_true * to, ku = e.acc_true * to;
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
       const int c = t.first + k * t.step, col = t.col0 + c;
       uint8_t* blk = st.base + (st.seq % kSlots) * kSlotBytes;
       if (!In::wait(st, t, k)) break;
-      uint32_t r[32], w[16];
+      uint32_t r[32], w[16], l[16];
       float v[32];
       block16_read(blk, st.lane, w);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 f = half2_bits_to_f32(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
-      block16_read(blk + 2048, st.lane, w);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 f = half2_bits_to_f32(w[i]);
-        v[2 * i] += f.x;
-        v[2 * i + 1] += f.y;
-      }
+      block16_read(blk + 2048, st.lane, l);
       src.load(c, r);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = __fmaf_rn(ei, v[i], __uint_as_float(r[i]) * e.acc_true);
+      for (int i = 0; i < 16; ++i) {
+        const float2 h = half2_bits_to_f32(w[i]), g = half2_bits_to_f32(l[i]);
+        v[2 * i] = __fmaf_rn(ei, h.x, __fmaf_rn(ei, g.x, __uint_as_float(r[2 * i]) * ku));
+        v[2 * i + 1] =
+            __fmaf_rn(ei, h.y, __fmaf_rn(ei, g.y, __uint_as_float(r[2 * i + 1]) * ku));
+      }
       __syncwarp();  // the whole block was read
       if (!e.out) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= e.to_Y;
         ortho_store(st, m, t, blk, col, v, true, false);
       } else {
 #pragma unroll
