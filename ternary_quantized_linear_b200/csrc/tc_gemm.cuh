@@ -16,7 +16,7 @@
 // MMA work; CG = 1 is for outputs with few tiles.  An SM takes 64 bytes a
 // cycle from L2, and a 64-k step of a 256 x 256 pair tile needs 32 KiB per SM
 // and 512 cycles of MMA: both just meet, while a 128 x 128 tile, with as many
-// bytes for half the MMA work, runs at half the rate.  SPLIT = 2 or 4
+// bytes for half the MMA work, runs at half the rate.  SPLIT = 2 to 4
 // (CG = 1) lets a cluster of CTAs share one tile's contraction: each sums its
 // part, the parts meet through distributed shared memory, added in rank
 // order, and each CTA finishes its share of the columns.
@@ -456,19 +456,17 @@ struct TgTmemSrc {
   }
 };
 
-// Parts of a cluster's CTAs, [SPLIT][columns of this CTA][128 rows] fp32 in
-// this CTA's shared memory, added in rank order.
+// Parts of a cluster's CTAs of one chunk, [SPLIT][32 columns][128 rows] fp32
+// in this CTA's shared memory, added in rank order.
 template <int SPLIT>
 struct TgClusterSrc {
   const float* parts;  // of this thread's row
-  int first;           // the CTA's first column of the tile
-  __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
-    const float* at = parts + (c - first) * 128;
+  __device__ __forceinline__ void load(int, uint32_t (&r)[32]) const {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      float v = at[i * 128];
+      float v = parts[i * 128];
 #pragma unroll
-      for (int s = 1; s < SPLIT; ++s) v = __fadd_rn(v, at[s * (128 / SPLIT) * 128 + i * 128]);
+      for (int s = 1; s < SPLIT; ++s) v = __fadd_rn(v, parts[s * 4096 + i * 128]);
       r[i] = __float_as_uint(v);
     }
   }
@@ -495,7 +493,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
 tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
                const typename Epi::Params ep) {
   using C = TgCfg<CG, BN, Epi>;
-  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::RING_BYTES >= 131072), "split");
+  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::RING_BYTES >= 65536 + ((3 + SPLIT) / SPLIT) * SPLIT * 16384),
+                "split");
   extern __shared__ uint8_t tg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(tg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -710,7 +709,7 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         Epi::run(ep, p, maps, t, st, TgTmemSrc{lanes});
       } else {
         Epi::run(ep, p, maps, t, st,
-                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem), 0});
+                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem)});
       }
       st.seq = 0;
     }
@@ -759,26 +758,25 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   }
   __syncwarp();
   if constexpr (SPLIT > 1) {
-    // One tile per cluster: CTA r finishes columns [128 r / SPLIT, 128 (r + 1)
-    // / SPLIT), a chunk of 32 per warp.  The ring's first half holds this
-    // CTA's part, its second half receives the CTA's columns of every part.
-    constexpr int kChunks = 4 / SPLIT;
-    constexpr uint32_t kShare = 65536 / SPLIT;
+    // One tile per cluster: CTA r finishes the chunks of 32 columns r and, if
+    // there is one, r + SPLIT, one per half of its warps.  The ring's first 64
+    // KiB hold this CTA's part, behind them it receives its chunks of every part.
+    constexpr uint32_t kChunk = 16384;  // bytes: 32 columns, 128 rows
+    const int mine = static_cast<int>(rank) + SPLIT < 4 ? 2 : 1;
     fence_proxy_async_smem();
     __syncthreads();
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(parts_bar, 65536);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(parts_bar, mine * SPLIT * kChunk);
     cluster_sync();
     if (threadIdx.x == 0) {
       const uint32_t base = smem_u32(smem);
 #pragma unroll
-      for (int s = 0; s < SPLIT; ++s)
-        dsmem_copy(map_to_rank(base + 65536u + rank * kShare, s), base + s * kShare, kShare,
-                   map_to_rank(smem_u32(parts_bar), s));
+      for (uint32_t c = 0; c < 4; ++c)
+        dsmem_copy(map_to_rank(base + 65536u + ((c / SPLIT) * SPLIT + rank) * kChunk, c % SPLIT),
+                   base + c * kChunk, kChunk, map_to_rank(smem_u32(parts_bar), c % SPLIT));
     }
-    const TgPart whole = part_of(tg_tile(p, worker), q, half);
-    if (warp >= 4 && half < kChunks) {
-      TgPart part = whole;
-      part.first = 32 * (static_cast<int>(rank) * kChunks + half);
+    if (warp >= 4 && half < mine) {
+      TgPart part = part_of(tg_tile(p, worker), q, half);
+      part.first = 32 * (static_cast<int>(rank) + half * SPLIT);
       part.step = 1 << 20;
       const bool run = *abort_flag == 0;
       if (run) Epi::begin(st, maps, ep, p, part);
@@ -787,8 +785,8 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       if (!ok && lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
       if (run && ok)
         Epi::run(ep, p, maps, part, st,
-                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem) + 16384 + 32 * q + lane,
-                                     static_cast<int>(rank) * 32 * kChunks});
+                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem) + 16384 +
+                                     half * SPLIT * 4096 + 32 * q + lane});
       else if (run)
         Epi::abandon(st, ep, part);
     }

@@ -98,31 +98,33 @@ int64_t tg_tiles(int64_t M, int64_t N, int64_t batch, bool sym, int bm, int bn) 
 }
 
 // Cycles that a plan needs, roughly: its waves of tiles, a tile's steps and
-// its epilogue.  A pair's 64-k step takes 660 cycles (measured; the MMAs
-// alone 512), a 128 x 128 step 680 (32 KiB at 64 bytes a cycle are 512; the
+// its epilogue.  A pair's 64-k step takes 650 cycles (measured; the MMAs
+// alone 512), a 128 x 128 step 570 (32 KiB at 64 bytes a cycle are 512; the
 // MMAs 256); the epilogue and what a launch waits for come on top of each
-// wave, and for a cluster's split the meeting of the parts (3 us).  Of clusters of
-// two SMs 74 are resident at a time, of four 33 (the occupancy query's answer
-// on a B200: its SM groups do not divide into fours).
+// wave, and for a cluster's split the meeting of the parts (4 us).  Of clusters
+// of two SMs 74 are resident at a time, of three 45, of four 33 (the occupancy
+// query's answer on a B200: its SM groups do not divide into fours).
 double tg_cost(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, const TgPlan& pl) {
   const int64_t tiles = tg_tiles(M, N, batch, sym, 128 * pl.cg, pl.bn);
-  const int64_t slots = pl.split == 4 ? 33 : kPlanSms / std::max(pl.cg, pl.split);
+  const int64_t slots = pl.split == 4   ? 33
+                        : pl.split == 3 ? 45
+                                        : kPlanSms / std::max(pl.cg, pl.split);
   const double waves = static_cast<double>(ceil_div(tiles, slots));
-  if (pl.cg == 2) return waves * (660.0 * static_cast<double>(steps) + 5000.0);
-  return waves * (680.0 * static_cast<double>(ceil_div(steps, pl.split)) + 3000.0 +
-                  (pl.split > 1 ? 5500.0 : 0.0));
+  if (pl.cg == 2) return waves * (650.0 * static_cast<double>(steps) + 5000.0);
+  return waves * (570.0 * static_cast<double>(ceil_div(steps, pl.split)) + 3000.0 +
+                  (pl.split > 1 ? 7000.0 : 0.0));
 }
 
 // Pairs on 256 x 256 tiles, or single SMs on 128 x 128 tiles, each tile's
-// steps shared by a cluster of up to max_split CTAs: whichever tg_cost
-// prefers.  Every CTA of a cluster needs a step of its own.
+// steps shared by a cluster of one of the sizes in `splits` (a bit each):
+// whichever tg_cost prefers.  Every CTA of a cluster needs a step of its own.
 TgPlan tg_plan(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, int passes,
-               int max_split) {
+               unsigned splits) {
   TgPlan best{2, 256, 1};
   double cost = tg_cost(M, N, batch, sym, steps * passes, best);
-  for (int s = 1; s <= max_split; s *= 2) {
+  for (int s = 1; s <= 4; ++s) {
+    if (!(splits >> s & 1u) || (s - 1) * ceil_div(steps, s) >= steps) continue;
     const TgPlan pl{1, 128, s};
-    if ((s - 1) * ceil_div(steps, s) >= steps) continue;
     const double c = tg_cost(M, N, batch, sym, ceil_div(steps, s) * s * passes, pl);
     if (c < cost) {
       cost = c;
@@ -131,6 +133,8 @@ TgPlan tg_plan(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, int
   }
   return best;
 }
+constexpr unsigned kNoSplit = 1u << 1, kSplit124 = 1u << 1 | 1u << 2 | 1u << 4,
+                   kSplit1234 = kSplit124 | 1u << 3;
 
 // Resident workers (pairs or single CTAs) of one kernel instance, per device;
 // sets the kernel's shared-memory limit the first time.
@@ -272,6 +276,11 @@ bitnet_status launch_tg_split(const DeviceState& ds, const TgProblem& g,
                               const typename Epi::Params& ep, cudaStream_t stream,
                               TgReady* ready) {
   switch (g.plan.split) {
+    case 3:
+      // (only X X^T's epilogue leaves the ring room for three parts of two chunks)
+      if constexpr (TgCfg<1, 128, Epi>::RING_BYTES >= 163840)
+        return launch_tg_cfg<1, 128, 3, Epi>(ds, g, ep, stream, ready);
+      return BITNET_ERR_INVALID_ARG;
     case 2: return launch_tg_cfg<1, 128, 2, Epi>(ds, g, ep, stream, ready);
     case 4: return launch_tg_cfg<1, 128, 4, Epi>(ds, g, ep, stream, ready);
     default: return launch_tg<128, Epi>(ds, g, ep, stream, ready);
@@ -309,7 +318,7 @@ bitnet_status check_ce_shape(int64_t M, int64_t V, int64_t K) {
 // columns evenly over all of them (a multiple of `unit`).
 TgPlan ce_logits_plan(int64_t M, int64_t cols, int64_t K, int unit) {
   if (M > 128) {
-    const TgPlan pl = tg_plan(M, cols, 1, false, ceil_div(K, kTgKStep), 1, 1);
+    const TgPlan pl = tg_plan(M, cols, 1, false, ceil_div(K, kTgKStep), 1, kNoSplit);
     return pl;
   }
   const int64_t rounds = ceil_div(cols, 256LL * kPlanSms);
@@ -700,7 +709,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.M = cols;
       g.N = K;
       g.Kc = M;
-      g.plan = tg_plan(cols, K, 1, false, ceil_div(M, kTgKStep), 1, 1);
+      g.plan = tg_plan(cols, K, 1, false, ceil_div(M, kTgKStep), 1, kNoSplit);
       st = launch_tg<128, TgStoreBf16>(*ds, g, TgStoreBf16::Params{scale}, s);
       if (st != BITNET_OK) return st;
     }
@@ -780,9 +789,9 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
 
   const int passes = L.split ? 3 : 1;
   const int64_t n_steps = ceil_div(L.n, kTgKStep), k_steps = ceil_div(L.k, kTgKStep);
-  const TgPlan gram_plan = tg_plan(L.n, L.n, B, !L.split, k_steps, passes, 4);
-  const TgPlan poly_plan = tg_plan(L.n, L.n, B, !L.split, n_steps, passes, 4);
-  const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes, 4);
+  const TgPlan gram_plan = tg_plan(L.n, L.n, B, !L.split, k_steps, passes, kSplit1234);
+  const TgPlan poly_plan = tg_plan(L.n, L.n, B, !L.split, n_steps, passes, kSplit124);
+  const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes, kSplit124);
   // The result goes out by TMA where its rows are whole 16-byte pieces.
   const bool direct = !tall && L.k % 8 != 0;
   TgReady gram_ready[2], poly_ready, update_ready[2], last_ready;
