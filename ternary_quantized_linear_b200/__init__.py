@@ -9,6 +9,7 @@ CPU fallback: if the library is missing or a call fails, an exception is
 raised.
 """
 import ctypes
+import functools
 import os
 import threading
 
@@ -734,7 +735,7 @@ def _on(device, stream, run):
     if stream is None:
         if torch.cuda.current_device() == device.index:
             # (the current stream's pointer without building a Stream object)
-            return run(ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index)))
+            return run(torch._C._cuda_getCurrentRawStream(device.index))
         with torch.cuda.device(device):
             return run(_stream())
     if stream.device != device:
@@ -743,10 +744,23 @@ def _on(device, stream, run):
         return run(_stream(stream))
 
 
-def _same_device(first, *ts):
+def _need_one_device(first, *ts):
+    """Contiguous CUDA tensors, all on one device."""
+    _need_cuda(first, *ts)
+    device = first.device
     for t in ts:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors must be on one device, got {first.device} and {t.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors must be on one device, got {device} and {t.device}")
+    return device
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, *sizes):
+    return int(getattr(load_library(), name)(*sizes))
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(workspace, nbytes, device):
@@ -757,13 +771,14 @@ def _scratch(workspace, nbytes, device):
 def _expect_head(x, W, targets):
     _expect(x, "x", torch.bfloat16)
     _expect(W, "W", torch.bfloat16)
-    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+    sx, sw = x.shape, W.shape
+    if len(sx) != 2 or len(sw) != 2 or sx[1] != sw[1]:
         raise ValueError("x must be [M, K] and W [V, K]")
-    M, K = x.shape
+    M, K = sx
     _expect(targets, "targets", torch.int64, shape=(M,))
     if K < 8 or K % 8:
         raise ValueError(f"K must be a multiple of 8, got {K}")
-    return M, W.shape[0], K
+    return M, sw[0], K
 
 
 def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=None, stream=None):
@@ -775,21 +790,18 @@ def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=N
     for t, name in ((loss, "loss"), (lse, "lse")):
         if t is not None:
             _expect(t, name, torch.float32, shape=(M,))
-    lib = load_library()
-    nb = int(lib.bitnet_cross_entropy_forward_workspace_bytes(M, V, K))
+    nb = _workspace_bytes("bitnet_cross_entropy_forward_workspace_bytes", M, V, K)
     if workspace is not None:
         _expect(workspace, "workspace", torch.uint8, numel=nb)
-    _need_cuda(x, W, targets, loss, lse, workspace)
-    _same_device(x, W, targets, loss, lse, workspace)
-    dev = x.device
+    dev = _need_one_device(x, W, targets, loss, lse, workspace)
 
     def run(handle):
         y = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
         z = torch.empty(M, dtype=torch.float32, device=dev) if lse is None else lse
         ws = _scratch(workspace, nb, dev)
-        _check("bitnet_cross_entropy_forward", lib.bitnet_cross_entropy_forward(
-            _ptr(x), _ptr(W), _ptr(targets), M, V, K, _ptr(y), _ptr(z), _ptr(ws), ws.numel(),
-            handle))
+        _check("bitnet_cross_entropy_forward", load_library().bitnet_cross_entropy_forward(
+            x.data_ptr(), W.data_ptr(), targets.data_ptr(), M, V, K, y.data_ptr(), z.data_ptr(),
+            ws.data_ptr(), ws.numel(), handle))
         return y, z
 
     return _on(dev, stream, run)
@@ -808,13 +820,10 @@ def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_
         _expect(dx, "dx", torch.bfloat16, shape=(M, K))
     if dW is not None:
         _expect(dW, "dW", torch.bfloat16, shape=(V, K))
-    lib = load_library()
-    nb = int(lib.bitnet_cross_entropy_backward_workspace_bytes(M, V, K))
+    nb = _workspace_bytes("bitnet_cross_entropy_backward_workspace_bytes", M, V, K)
     if workspace is not None:
         _expect(workspace, "workspace", torch.uint8, numel=nb)
-    _need_cuda(x, W, targets, lse, dloss, dx, dW, workspace)
-    _same_device(x, W, targets, lse, dloss, dx, dW, workspace)
-    dev = x.device
+    dev = _need_one_device(x, W, targets, lse, dloss, dx, dW, workspace)
 
     def run(handle):
         gx, gW = dx if need_dx else None, dW if need_dW else None
@@ -823,9 +832,9 @@ def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_
         if gW is None and need_dW:
             gW = torch.empty(V, K, dtype=torch.bfloat16, device=dev)
         ws = _scratch(workspace, nb, dev)
-        _check("bitnet_cross_entropy_backward", lib.bitnet_cross_entropy_backward(
-            _ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K, _ptr(gx), _ptr(gW),
-            _ptr(ws), ws.numel(), handle))
+        _check("bitnet_cross_entropy_backward", load_library().bitnet_cross_entropy_backward(
+            x.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), M,
+            V, K, _address(gx), _address(gW), ws.data_ptr(), ws.numel(), handle))
         return gx, gW
 
     return _on(dev, stream, run)
@@ -859,20 +868,18 @@ def bitnet_orthogonalize(U, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, ep
     flat = [float(c) for row in rows for c in row]
     if out is not None:
         _expect(out, "out", torch.bfloat16, shape=tuple(U.shape))
-    lib = load_library()
-    nb = int(lib.bitnet_orthogonalize_workspace_bytes(B, N, K))
+    nb = _workspace_bytes("bitnet_orthogonalize_workspace_bytes", B, N, K)
     if workspace is not None:
         _expect(workspace, "workspace", torch.uint8, numel=nb)
-    _need_cuda(U, out, workspace)
-    _same_device(U, out, workspace)
-    dev = U.device
+    dev = _need_one_device(U, out, workspace)
 
     def run(handle):
         O = torch.empty(tuple(U.shape), dtype=torch.bfloat16, device=dev) if out is None else out
         ws = _scratch(workspace, nb, dev)
-        _check("bitnet_orthogonalize", lib.bitnet_orthogonalize(
-            _ptr(U), _dtype_code(U.dtype), B, N, K, steps, (ctypes.c_double * (3 * steps))(*flat),
-            ctypes.c_float(eps), _ptr(O), _ptr(ws), ws.numel(), handle))
+        _check("bitnet_orthogonalize", load_library().bitnet_orthogonalize(
+            U.data_ptr(), _dtype_code(U.dtype), B, N, K, steps,
+            (ctypes.c_double * (3 * steps))(*flat), eps, O.data_ptr(), ws.data_ptr(), ws.numel(),
+            handle))
         return O
 
     return _on(dev, stream, run)
