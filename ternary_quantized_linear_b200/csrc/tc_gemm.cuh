@@ -96,6 +96,7 @@ struct TgShape {
   int tiles;             // all: batch * per_batch * ksplit
   int sym;               // only tiles with m >= n (square output)
   int group;             // m tiles that share one sweep over n
+  int backwards;         // the contraction runs from its end
   int passes;
   uint32_t idesc;
   int* status;
@@ -613,8 +614,9 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
             uint32_t bar = smem_u32(&full[s]);
             if (CG == 2) bar = map_to_rank(bar, 0);
             if (half_rank == 0) mbar_arrive_expect_tx(&full[s], stage_tx);
-            tg_load<CG, Epi::kAMn>(ma, a_rows, dst, a0, j * kTgKStep, tile.b, bar);
-            tg_load<CG, Epi::kBMn>(mb, b_rows, dst + a_bytes, b0, j * kTgKStep, tile.b, bar);
+            const int k0 = (p.backwards ? k_hi - 1 - (j - k_lo) : j) * kTgKStep;
+            tg_load<CG, Epi::kAMn>(ma, a_rows, dst, a0, k0, tile.b, bar);
+            tg_load<CG, Epi::kBMn>(mb, b_rows, dst + a_bytes, b0, k0, tile.b, bar);
             if (++s == stages) {
               s = 0;
               ++round;
