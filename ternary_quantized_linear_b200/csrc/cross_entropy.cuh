@@ -11,8 +11,8 @@
 // columns, the running maximum and the sum of exp(z - maximum) (fp32) of all
 // but the target's logit; a second kernel joins them.  The logits never leave
 // the SM.  The target's logit is a dot product of its own, in fp32 with
-// rounded sums (the tensor cores truncate theirs, which at 4096 terms moves a
-// logit by some 1e-6 of itself): with s the sum of exp(z_v - z_t) over the
+// rounded sums (the tensor cores truncate theirs, which at 4096 terms of one
+// sign makes a logit 1e-5 of itself too small): with s the sum of exp(z_v - z_t) over the
 // others, loss = log(1 + s) has no cancellation for a confident token, and
 // the target's entry of the gradient is exp(z_t - lse) - 1 by expm1.
 // Backward: the vocabulary is taken in pieces; the same product forms g of a
@@ -62,9 +62,15 @@ __device__ __forceinline__ float ce_target_dot(const __nv_bfloat16* __restrict__
   return s;
 }
 
+// The statistics of a row over half a tile's columns, the target's left out.
+// On single SMs the tensor cores sum runs of 8 steps, 512 terms: 100 tokens
+// over 2000 x 4096, all terms positive, lse off by 1.4e-5 instead of 4.4e-4,
+// and one token's loss by 1e-7 of itself instead of 1e-6, in the same time
+// (48.5 us over 32000 x 4096).  CeGrad forms its logits the same way: e^(z - lse)
+// wants both off alike.
 struct CeStats {
   static constexpr bool kAMn = false, kBMn = false, kBf16 = true;
-  static constexpr int kSlots = 0, kSlotBytes = 0;
+  static constexpr int kRun = 8, kSlots = 0, kSlotBytes = 0;
   struct Params {
     const int64_t* targets;
     float2* part;          // [2 nt][M]: maximum, sum of exp(z - maximum)
@@ -256,7 +262,7 @@ ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __res
 
 struct CeGrad {
   static constexpr bool kAMn = false, kBMn = false, kBf16 = true;
-  static constexpr int kSlots = 2, kSlotBytes = 2048;
+  static constexpr int kRun = CeStats::kRun, kSlots = 2, kSlotBytes = 2048;
   struct Params {
     const int64_t* targets;
     const float* lse;

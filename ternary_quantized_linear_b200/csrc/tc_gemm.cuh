@@ -36,6 +36,14 @@
 // arrive, about 5 us; the epilogue warps take that pass on an empty tile
 // (`dry`) while the first copies and MMAs are under way.
 //
+// The tensor cores truncate every sum: 16 terms at a time, half a unit of the
+// last place off toward zero on average, so a logit of 4096 terms comes out
+// some 1e-5 of itself too small.  An epilogue that needs better (kRun) has the
+// contraction in runs of so many steps on single SMs, which its warps add up
+// with rounding in the second accumulator; where few rows leave the tensor
+// cores waiting for memory that costs nothing.  Pairs have no accumulator to
+// spare, and take contractions whole.
+//
 // A product of fewer than 128 rows copies only those (rounded up to 8): the
 // MMA then takes whatever follows in the ring for the missing rows, whose sums
 // nobody reads, and the ring holds more stages.  Reading a head for one token
@@ -457,6 +465,33 @@ struct TgTmemSrc {
   }
 };
 
+// The last run of a contraction and the sum of those before it (none: !more).
+struct TgRunSrc {
+  uint32_t addr, sum;
+  bool more;
+  __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
+    TgTmemSrc{addr}.load(c, r);
+    if (more) {
+      uint32_t s[32];
+      TgTmemSrc{sum}.load(c, s);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        r[i] = __float_as_uint(__fadd_rn(__uint_as_float(s[i]), __uint_as_float(r[i])));
+    }
+  }
+  // Add this run to the sum: the columns of a part.
+  __device__ __forceinline__ void add(const TgPart& t) const {
+    const int n = t.any ? t.chunks() : 0;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      uint32_t r[32];
+      load(t.first + k * t.step, r);
+      tmem_st_32x32b_x32(sum + t.first + k * t.step, r);
+    }
+    tmem_st_wait();
+  }
+};
+
 // Parts of a cluster's CTAs of one chunk, [SPLIT][32 columns][128 rows] fp32
 // in this CTA's shared memory, added in rank order.
 template <int SPLIT>
@@ -486,7 +521,7 @@ __device__ __forceinline__ void dsmem_copy(uint32_t dst_cluster, uint32_t src, u
 // ------------------------------------------------------------------- kernel
 
 // Epi: struct with Params, kAMn and kBMn (which operands are MN-major) and
-// kBf16 (else fp16), kSlots, kSlotBytes, begin(...) (called before the
+// kBf16 (else fp16), kRun, kSlots, kSlotBytes, begin(...) (called before the
 // accumulator is waited for), run(...), which takes the part's chunks, and
 // abandon(...) for a part that was begun and is not run.
 template <int CG, int BN, int SPLIT, class Epi>
@@ -510,6 +545,9 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int CLUSTER = CG * SPLIT;
+  // Steps that the tensor cores sum before the epilogue warps add the run up
+  // (then one accumulator holds the run, the other the sum); 0: all of them.
+  constexpr int RUN = CG == 1 && SPLIT == 1 ? Epi::kRun : 0;
   const uint32_t rank = CLUSTER > 1 ? cluster_rank() : 0u;
   const uint32_t half_rank = CG == 2 ? rank : 0u;  // which half of the pair's tile
   const uint64_t limit = p.wait_limit_ns;
@@ -657,42 +695,48 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       uint32_t s = 0, ph = 0;
       int local = 0;
       bool ok = true;
-      for (int t = worker; t < p.tiles && ok; t += workers, ++local) {
-        const int buf = local & 1;
+      for (int t = worker; t < p.tiles && ok; t += workers) {
         int k_lo, k_hi;
         k_range(p.ksplit > 1 ? t % p.ksplit : 0, k_lo, k_hi);
         const int n_it = (k_hi - k_lo) * p.passes;
-        if (local >= 2 && !mbar_wait_bounded(&accempty[buf],
-                                             static_cast<uint32_t>((local >> 1) - 1) & 1u,
-                                             abort_flag, limit)) {
-          *abort_flag = 1;
-          record_failure(p.status, DEV_TIMEOUT_MMA);
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-        for (int j = 0; j < n_it; ++j) {
-          if (!mbar_wait_bounded(&full[s], ph, abort_flag, limit)) {
+        int j = 0;
+        do {
+          const int buf = RUN > 0 ? 0 : local & 1;
+          const int start = RUN > 0 ? j : 0, end = RUN > 0 ? min(n_it, j + RUN) : n_it;
+          const bool used = local >= (RUN > 0 ? 1 : 2);
+          const uint32_t before = static_cast<uint32_t>(RUN > 0 ? local - 1 : (local >> 1) - 1);
+          if (used && !mbar_wait_bounded(&accempty[buf], before & 1u, abort_flag, limit)) {
             *abort_flag = 1;
             record_failure(p.status, DEV_TIMEOUT_MMA);
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          // (start addresses stay below 2^18: adding to the field is safe)
-          const uint64_t at = s * (stage_bytes >> 4);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+          for (; j < end; ++j) {
+            if (!mbar_wait_bounded(&full[s], ph, abort_flag, limit)) {
+              *abort_flag = 1;
+              record_failure(p.status, DEV_TIMEOUT_MMA);
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            // (start addresses stay below 2^18: adding to the field is safe)
+            const uint64_t at = s * (stage_bytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kTgKStep / 16; ++kk)
-            tg_mma<CG>(d, desc_a + at + (Epi::kAMn ? 128 : 2) * kk,
-                       desc_b + at + (Epi::kBMn ? 128 : 2) * kk, idesc,
-                       (kk > 0 || j > 0) ? 1u : 0u);
-          tg_commit<CG>(&empty[s]);
-          if (++s == stages) {
-            s = 0;
-            ph ^= 1u;
+            for (int kk = 0; kk < kTgKStep / 16; ++kk)
+              tg_mma<CG>(d, desc_a + at + (Epi::kAMn ? 128 : 2) * kk,
+                         desc_b + at + (Epi::kBMn ? 128 : 2) * kk, idesc,
+                         (kk > 0 || j > start) ? 1u : 0u);
+            tg_commit<CG>(&empty[s]);
+            if (++s == stages) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
-        }
-        if (ok) tg_commit<CG>(&accfull[buf]);
+          if (ok) tg_commit<CG>(&accfull[buf]);
+          ++local;
+        } while (RUN > 0 && ok && j < n_it);
       }
       if (*abort_flag) {  // the MMAs issued so far still read shared memory
         tg_commit<CG>(drain);
@@ -708,7 +752,10 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       t.first = 0;
       t.col_end = min(t.col_end, 32);
       if constexpr (SPLIT == 1) {
-        Epi::run(ep, p, maps, t, st, TgTmemSrc{lanes});
+        if constexpr (RUN > 0)
+          Epi::run(ep, p, maps, t, st, TgRunSrc{lanes, lanes + BN, false});
+        else
+          Epi::run(ep, p, maps, t, st, TgTmemSrc{lanes});
       } else {
         Epi::run(ep, p, maps, t, st,
                  TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem)});
@@ -719,11 +766,29 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
     pdl_wait_prior_grid();
     int local = 0;
     for (int t = worker; t < p.tiles; ++local) {
-      const int buf = local & 1;
+      const int buf = RUN > 0 ? 0 : local & 1;
       if constexpr (SPLIT == 1) Epi::begin(st, maps, ep, p, part);
-      const bool ok = __all_sync(
-          0xFFFFFFFFu, mbar_wait_bounded(&accfull[buf], static_cast<uint32_t>(local >> 1) & 1u,
-                                         abort_flag, limit));
+      auto summed = [&]() {
+        const int turn = RUN > 0 ? local : local >> 1;
+        return __all_sync(0xFFFFFFFFu,
+                          mbar_wait_bounded(&accfull[buf], static_cast<uint32_t>(turn) & 1u,
+                                            abort_flag, limit));
+      };
+      bool ok = true, more = false;
+      if constexpr (RUN > 0) {
+        for (int j = RUN; j < p.steps && ok; j += RUN) {  // all runs but the last
+          ok = summed();
+          if (!ok) break;
+          tc_fence_after_sync();
+          TgRunSrc{lanes, lanes + BN, more}.add(part);
+          more = true;
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&accempty[0]);
+          ++local;
+        }
+      }
+      ok = ok && summed();
       if (!ok) {
         *abort_flag = 1;
         if (lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
@@ -733,7 +798,10 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
       tc_fence_after_sync();
       const uint32_t acc = lanes + static_cast<uint32_t>(buf * BN);
       if constexpr (SPLIT == 1) {
-        Epi::run(ep, p, maps, part, st, TgTmemSrc{acc});
+        if constexpr (RUN > 0)
+          Epi::run(ep, p, maps, part, st, TgRunSrc{acc, acc + BN, more});
+        else
+          Epi::run(ep, p, maps, part, st, TgTmemSrc{acc});
       } else {
         // This CTA's part, [column][row] fp32, over the ring (all consumed).
         float* part_sum = reinterpret_cast<float*>(smem);
@@ -824,7 +892,7 @@ __device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensor
 // 32000 x 2048 at 2.9 TB/s; a plain fill of that size reaches 3.5).
 struct TgStoreBf16 {
   static constexpr bool kAMn = true, kBMn = true, kBf16 = true;
-  static constexpr int kSlots = 2, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kSlots = 2, kSlotBytes = 4096;
   struct Params {
     const float* scale;
   };
@@ -863,7 +931,7 @@ struct TgStoreBf16 {
 // a split contraction goes to its own [M][N] of the output.
 struct TgAccumulate {
   static constexpr bool kAMn = false, kBMn = true, kBf16 = true;
-  static constexpr int kSlots = 3, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kSlots = 3, kSlotBytes = 4096;
   struct Params {
     int add;             // add `in`
     int to_bf16;         // `out` is bf16 (else fp32)

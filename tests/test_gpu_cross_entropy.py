@@ -278,3 +278,25 @@ def test_cross_entropy_refuses_strided_tensors():
         flat = torch.zeros(4 * 64 + 1, dtype=torch.bfloat16, device="cuda")
         tql.bitnet_cross_entropy_forward(flat[1:].view(4, 64), W, t)
     assert e.value.code == tql.BITNET_ERR_MISALIGNED
+
+
+@pytest.mark.parametrize("M", [1, 100])
+def test_few_rows_sum_in_short_runs(M):
+    """All terms positive, so that truncated sums err one way: the tensor cores
+    sum 512 terms at a time.  A run's 32 truncations lose less than 2^-23 of
+    the sum so far each, 16.5 * 2^-23 of the run together; the eight runs join
+    with seven roundings.  (4096 terms in one go would lose up to 128 * 2^-23,
+    about a third of it in the mean.)"""
+    V, K = 2000, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (0.5 + torch.rand((M, K), generator=g, device="cuda")).bfloat16()
+    W = (0.005 + 0.01 * torch.rand((V, K), generator=g, device="cuda")).bfloat16()
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    lse = tql.bitnet_cross_entropy_forward(x, W, t)[1].double()
+    z = x.double() @ W.double().T
+    exact = torch.logsumexp(z, 1)
+    # the target's own logit (K/32 + 16 roundings) counts by its share of the sum
+    share = torch.exp(z.amax(1) - exact) * (K / 32 + 16) * 2.0 ** -24
+    tol = (z.amax(1) * (16.5 * 2.0 ** -23 + 7 * 2.0 ** -24 + share) + 2.0 ** -23 * exact
+           + 2.0 ** -22 * (1 + z.amax(1)) + 200 * 2.0 ** -24)
+    assert ((lse - exact).abs() <= tol).all(), ((lse - exact).abs() / tol).max()
