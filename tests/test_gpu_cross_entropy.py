@@ -300,3 +300,13 @@ def test_few_rows_sum_in_short_runs(M):
     tol = (z.amax(1) * (16.5 * 2.0 ** -23 + 7 * 2.0 ** -24 + share) + 2.0 ** -23 * exact
            + 2.0 ** -22 * (1 + z.amax(1)) + 200 * 2.0 ** -24)
     assert ((lse - exact).abs() <= tol).all(), ((lse - exact).abs() / tol).max()
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 90000, 1032), (64, 40001, 1544), (128, 39000, 1024),
+                                   (200, 700, 1096)])
+def test_runs_over_several_tiles(M, V, K):
+    """More tiles than SMs, each of more than one run (the last one short)."""
+    x, W, t, d = _inputs(M, V, K, seed=M + V, sigma=0.02)
+    exact, tol = _exact(x, W, t, d)
+    _check(_run(x, W, t, d), exact, tol)
+    assert tql.bitnet_device_status(reset=False) == (tql.BITNET_OK, 0)
