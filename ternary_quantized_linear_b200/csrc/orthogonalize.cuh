@@ -481,7 +481,7 @@ struct OrthoUpdate {
 
 // ------------------------------------------------- small updates in one launch
 
-// n <= 128 and k <= 2048: all steps in one launch, X, R and Q in shared
+// n <= 128 and k <= 4096: all steps in one launch, X, R and Q in shared
 // memory.  Sixteen launches of a few microseconds of latency each were 150 us
 // for a 128 x 128 update whose products take 5.
 //
@@ -497,6 +497,7 @@ struct OrthoUpdate {
 
 constexpr int kOsThreads = 512;
 constexpr int kOsMaxKs = 256;
+constexpr int kOsMaxCluster = 16;
 
 struct OsStep {
   float a, b, c;
@@ -522,8 +523,8 @@ struct OsSmem {
   static constexpr int OFF_R_LO = OFF_R + 32768;
   static constexpr int OFF_D = OFF_R + 65536;
   static constexpr int OFF_E = OFF_D + 512;
-  static constexpr int OFF_RED = OFF_E + 512;             // 16 + 8 doubles
-  static constexpr int OFF_BAR = OFF_RED + 192;           // MMAs, received rows
+  static constexpr int OFF_RED = OFF_E + 512;             // 16 + 16 doubles
+  static constexpr int OFF_BAR = OFF_RED + 256;           // MMAs, received rows
   static constexpr int SMEM_DYN = OFF_BAR + 32 + 1024;
   static_assert(SMEM_DYN <= 232448, "shared memory");
 };
@@ -768,22 +769,24 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(lanes + kGramCol + j, r);
         tmem_ld_wait();
-        const uint32_t owner = static_cast<uint32_t>(j / share);  // 16 columns, one owner
-        const uint32_t at = map_to_rank(
-            smem_u32(Rh) + static_cast<uint32_t>(
-                               ((static_cast<int>(rank) * share + j % share) * 32 + row) * 16),
-            owner);
-        // (column / 4) * 128 rows * 16 bytes = column * 512: 128 * 4 bytes a column
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 2048),
+        for (int i = 0; i < 4; ++i) {
+          const int o = (j + 4 * i) / share, at = (j + 4 * i) % share;
+          // (column / 4) * 128 rows * 16 bytes = column * 512: 128 * 4 bytes a column
+          const uint32_t to = map_to_rank(
+              smem_u32(Rh) + static_cast<uint32_t>(((static_cast<int>(rank) * share + at) * 32 +
+                                                    row) * 16),
+              static_cast<uint32_t>(o));
+          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to),
                        "r"(r[4 * i]), "r"(r[4 * i + 1]), "r"(r[4 * i + 2]), "r"(r[4 * i + 3])
                        : "memory");
+        }
       }
       os_sync(true);
       // The sums of this CTA's columns, in rank order; thread (row, grp) has
-      // share / 4 of them.
-      const int mine = share / 4, first = grp * mine;
+      // share / 4 of them, or four (and the last groups none).
+      const int each4 = max(4, share / 4), first = grp * each4;
+      const int mine = first < share ? each4 : 0;
       const float4* parts = reinterpret_cast<const float4*>(Rh);
       float sum[16];
 #pragma unroll

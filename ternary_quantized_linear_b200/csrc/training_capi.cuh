@@ -400,9 +400,16 @@ constexpr int kOrthoMaxSteps = 32;
 // Largest smaller side that runs on both halves of its operands.
 constexpr int64_t kOrthoSplitN = 192;
 
-// Updates that run in one launch on clusters of up to eight CTAs.
-bool ortho_is_small(int64_t N, int64_t K) {
-  return std::min(N, K) <= 128 && std::max(N, K) <= 8 * kOsMaxKs;
+// Updates that run in one launch: on clusters of up to eight CTAs, or of
+// sixteen, of which seven are resident at a time, for two rounds of them at
+// most (128 x 4096: 1 matrix 101 us, as products of their own 181; 7: 105 and
+// 210; 16: 305 and 268).
+constexpr int64_t kOsWideBatch = 14;
+
+bool ortho_is_small(int64_t B, int64_t N, int64_t K) {
+  const int64_t k = std::max(N, K);
+  return std::min(N, K) <= 128 &&
+         (k <= 8 * kOsMaxKs || (k <= kOsMaxCluster * kOsMaxKs && B <= kOsWideBatch));
 }
 
 bitnet_status check_ortho_shape(int64_t B, int64_t N, int64_t K) {
@@ -498,7 +505,13 @@ bitnet_status launch_ortho_small(const DeviceState& ds, const void* U, int u_bf1
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BITNET_ERR_CUDA;
   std::call_once(once[dev],
-                 [dev]() { ok[dev] = set_smem(ortho_small_kernel, OsSmem::SMEM_DYN); });
+                 [dev]() {
+                   // (clusters of sixteen are past the portable size)
+                   ok[dev] = set_smem(ortho_small_kernel, OsSmem::SMEM_DYN) &&
+                             cudaFuncSetAttribute(ortho_small_kernel,
+                                                  cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                                  1) == cudaSuccess;
+                 });
   if (!ok[dev]) return BITNET_ERR_CUDA;
   OsParams p{};
   p.U = U;
@@ -726,7 +739,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
 }
 
 BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K) {
-  if (check_ortho_shape(B, N, K) != BITNET_OK || B == 0 || ortho_is_small(N, K)) return 0;
+  if (check_ortho_shape(B, N, K) != BITNET_OK || B == 0 || ortho_is_small(B, N, K)) return 0;
   return ortho_layout(B, N, K).total;
 }
 
@@ -752,7 +765,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
   if (B == 0) return BITNET_OK;
   if (!U || !O) return BITNET_ERR_INVALID_ARG;
   if (!aligned(U, 16) || !aligned(O, 16)) return BITNET_ERR_MISALIGNED;
-  if (ortho_is_small(N, K)) {
+  if (ortho_is_small(B, N, K)) {
     DeviceState* ds = device_state();
     if (!ds) return BITNET_ERR_CUDA;
     return launch_ortho_small(*ds, U, u_dtype == BITNET_BF16 ? 1 : 0, B, N, K, steps,

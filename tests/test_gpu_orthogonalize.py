@@ -251,3 +251,15 @@ def test_a_training_step_together():
     assert (dW.double() - dW_want).norm() <= 1e-5 * dW_want.norm()
     _check(dW, O)
     assert dhead.shape == head.shape
+
+
+@pytest.mark.parametrize("B,N,K", [(1, 128, 4096), (1, 4096, 100), (2, 64, 3001), (1, 3, 2100),
+                                   (14, 128, 2500), (15, 128, 2500), (1, 100, 4104),
+                                   (1, 4100, 72), (1, 128, 8000)])
+def test_long_and_narrow(B, N, K):
+    """Clusters of sixteen (k up to 4096, more of them than fit at a time); past
+    them products with both halves, cut along a long contraction."""
+    U = _update(B, N, K, "lowrank", torch.bfloat16, seed=N + K)
+    got = tql.bitnet_orthogonalize(U)
+    for u, o in zip(U, got):
+        _check(u, o)

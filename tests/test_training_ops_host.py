@@ -105,7 +105,9 @@ def test_orthogonalize_refuses_bad_arguments(lib):
     assert lib.bitnet_orthogonalize_workspace_bytes(7, 128, 2048) == 0
     assert lib.bitnet_orthogonalize_workspace_bytes(7, 2048, 128) == 0
     assert lib.bitnet_orthogonalize_workspace_bytes(1, 129, 129) > 0
-    assert lib.bitnet_orthogonalize_workspace_bytes(1, 128, 2049) > 0
+    assert lib.bitnet_orthogonalize_workspace_bytes(14, 4096, 128) == 0
+    assert lib.bitnet_orthogonalize_workspace_bytes(15, 4096, 128) > 0
+    assert lib.bitnet_orthogonalize_workspace_bytes(1, 128, 4097) > 0
     assert lib.bitnet_orthogonalize_workspace_bytes(1, 0, 5) == 0
 
 
