@@ -412,6 +412,19 @@ bool ortho_is_small(int64_t B, int64_t N, int64_t K) {
          (k <= 8 * kOsMaxKs || (k <= kOsMaxCluster * kOsMaxKs && B <= kOsWideBatch));
 }
 
+// CTAs per matrix: one while it holds all columns; else four or eight of 128
+// columns each while the whole batch is resident (128 x 512: 2 CTAs 87 us, 4
+// 72; x 1024: 4 90, 8 76, 16 74; but 40 of the first 91 and 148, 30 of the
+// second 95 and 166); else as few as hold them.
+int ortho_small_cluster(int64_t B, int64_t k) {
+  if (k <= kOsMaxKs) return 1;
+  if (k <= 4 * 128 && B <= 33) return 4;
+  if (k > 4 * 128 && k <= 8 * 128 && B <= 15) return 8;
+  int cluster = 2;
+  while (cluster * kOsMaxKs < k) cluster *= 2;
+  return cluster;
+}
+
 bitnet_status check_ortho_shape(int64_t B, int64_t N, int64_t K) {
   if (B < 0 || N < 0 || K < 0) return BITNET_ERR_INVALID_ARG;
   const int64_t n = std::min(N, K), k = std::max(N, K);
@@ -520,8 +533,7 @@ bitnet_status launch_ortho_small(const DeviceState& ds, const void* U, int u_bf1
   p.n = static_cast<int>(std::min(N, K));
   p.k = static_cast<int>(std::max(N, K));
   p.tall = N > K ? 1 : 0;
-  p.cluster = 1;
-  while (p.cluster * kOsMaxKs < p.k) p.cluster *= 2;
+  p.cluster = ortho_small_cluster(B, p.k);
   p.ks = static_cast<int>(round_up(ceil_div(p.k, p.cluster), 64));
   p.steps = steps;
   p.eps = eps;

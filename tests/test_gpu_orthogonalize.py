@@ -263,3 +263,13 @@ def test_long_and_narrow(B, N, K):
     got = tql.bitnet_orthogonalize(U)
     for u, o in zip(U, got):
         _check(u, o)
+
+
+@pytest.mark.parametrize("B,N,K", [(1, 100, 257), (7, 128, 1025), (8, 1025, 128), (15, 64, 512),
+                                   (16, 64, 512), (34, 512, 40), (34, 20, 1024), (80, 33, 260)])
+def test_every_cluster_of_small_updates(B, N, K):
+    """Two to sixteen CTAs a matrix, by its columns and the batch."""
+    U = _update(B, N, K, "flat", torch.float32, seed=B + N + K)
+    got = tql.bitnet_orthogonalize(U)
+    for u, o in zip(U, got):
+        _check(u, o)
