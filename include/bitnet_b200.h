@@ -489,8 +489,9 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
  *   dx [M][K], dW [V][K] bf16, either may be NULL (not computed).
  *   All sums and the softmax's maximum, sum and logarithm are fp32; loss is
  *   log(1 + sum over the others of exp(z_v - z_t)), so a confident token's
- *   keeps its digits; g / max|dloss| is rounded to bf16 as an operand of the
- *   two gradient products.
+ *   keeps its digits; g / max|dloss| (over the finite ones of tokens with a
+ *   target) is rounded to bf16 as an operand of the two gradient products.  A
+ *   dloss of inf or NaN makes its own token's dx non-finite, and dW.
  *   Non-finite logits of a row give a non-finite or NaN lse and loss.
  *   M == 0: the forward queues nothing, the backward zeroes dW.
  * Shapes: K % 8 == 0, 8 <= K <= BITNET_MAX_K, 1 <= V <= BITNET_MAX_N,

@@ -21,10 +21,11 @@
 //
 // g is rounded to bf16 because it is a tensor-core operand next to bf16 x and
 // W (the MMA takes operands of one type, and fp16 cannot hold a weight's
-// range); every sum over it is fp32.  What is rounded is g / max|dloss|, the
-// common factor being put back in fp32 at the end: for a mean every dloss is
-// the same, and the entries of most tokens, near -1 from below, then round by
-// half as much as at an arbitrary factor's place between powers of two.
+// range); every sum over it is fp32.  What is rounded is g / max|dloss| (of the
+// finite ones), the common factor being put back in fp32 at the end: for a
+// mean every dloss is the same, and the entries of most tokens, near -1 from
+// below, then round by half as much as at an arbitrary factor's place between
+// powers of two.
 #pragma once
 
 #include "tc_gemm.cuh"
@@ -227,7 +228,8 @@ ce_join_kernel(const float2* __restrict__ part, int parts, const __nv_bfloat16* 
 }
 
 // Per row: the target's logit.  Block 0 also: max |dloss| over the rows that
-// have a target.
+// have a target and a finite one (1 where that is 0): an infinite dloss as the
+// common factor would make every other row 0 times infinity.
 __global__ void __launch_bounds__(256)
 ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ W,
                  const int64_t* __restrict__ targets, const float* __restrict__ dloss, int64_t M,
@@ -248,7 +250,10 @@ ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __res
   float a = 0.0f;
   for (int64_t m = threadIdx.x; m < M; m += 256) {
     const int64_t t = targets[m];
-    if (t >= 0 && t < V) a = fmaxf(a, fabsf(dloss[m]));  // NaN: its own row carries it
+    if (t >= 0 && t < V) {
+      const float d = fabsf(dloss[m]);
+      if (d < INFINITY) a = fmaxf(a, d);  // inf and NaN: their own rows carry them
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
@@ -256,7 +261,7 @@ ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __res
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 8; ++i) a = fmaxf(a, red[i]);
-    *scale = a;
+    *scale = a > 0.0f ? a : 1.0f;
   }
 }
 
@@ -268,7 +273,7 @@ struct CeGrad {
     const float* lse;
     const float* dloss;
     const float* logit;    // of the target
-    const float* scale;    // max |dloss|: g is formed relative to it
+    const float* scale;    // max finite |dloss|: g is formed relative to it
     int64_t V;             // of the whole vocabulary
     int64_t v0;            // first column of this piece
   };
@@ -283,7 +288,7 @@ struct CeGrad {
     float d = 0.0f, shift = 0.0f, at_target = 0.0f;
     if (valid) {
       const float dl = __ldg(e.dloss + t.row), l = __ldg(e.lse + t.row);
-      d = dl == 0.0f ? 0.0f : __fdiv_rn(dl, __ldcg(e.scale));
+      d = __fdiv_rn(dl, __ldcg(e.scale));
       shift = l * kLog2e;
       at_target = expm1f(__ldcg(e.logit + t.row) - l);
       target -= e.v0;

@@ -310,3 +310,31 @@ def test_runs_over_several_tiles(M, V, K):
     exact, tol = _exact(x, W, t, d)
     _check(_run(x, W, t, d), exact, tol)
     assert tql.bitnet_device_status(reset=False) == (tql.BITNET_OK, 0)
+
+
+def _close(got, exact, tol, tiny=2.0 ** -126):
+    """As _check, and a NaN is never close."""
+    for k, v in got.items():
+        off = (v.double() - exact[k]).abs()
+        assert (off <= tol[k] + tiny).all(), (k, off.max().item())
+
+
+@pytest.mark.parametrize("M,V,K", [(40, 300, 64), (300, 5003, 520)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_non_finite_upstream_gradients_stay_their_own(M, V, K, bad):
+    x, W, t, d = _inputs(M, V, K, seed=M)  # (tokens 1, 8, ... have no target)
+    exact, tol = _exact(x, W, t, d)
+    loss, lse = tql.bitnet_cross_entropy_forward(x, W, t)
+    d = d.clone()
+    d[[5, 20]] = bad
+    d[1] = bad  # of a token without loss: not looked at
+    dx, _ = tql.bitnet_cross_entropy_backward(x, W, t, lse, d, need_dW=False)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[[5, 20]] = False
+    _close({"dx": dx[keep]}, {"dx": exact["dx"][keep]}, {"dx": tol["dx"][keep]})
+    assert (dx[(t < 0) | (t >= V)] == 0).all()
+    assert not torch.isfinite(dx[5]).any() and not torch.isfinite(dx[20]).any()
+    # nothing finite but zeros: those rows still have no gradient
+    dx, _ = tql.bitnet_cross_entropy_backward(x, W, t, lse, torch.where(keep, 0.0, bad),
+                                              need_dW=False)
+    assert (dx[keep] == 0).all() and not torch.isfinite(dx[~keep]).any()
