@@ -492,7 +492,8 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
  *   keeps its digits; g / max|dloss| (over the finite ones of tokens with a
  *   target) is rounded to bf16 as an operand of the two gradient products.  A
  *   dloss of inf or NaN makes its own token's dx non-finite, and dW.
- *   Non-finite logits of a row give a non-finite or NaN lse and loss.
+ *   A logit of +inf or NaN gives its row a non-finite lse and loss.  One of
+ *   -inf has no weight; as the target it makes the loss inf, with lse as it is.
  *   M == 0: the forward queues nothing, the backward zeroes dW.
  * Shapes: K % 8 == 0, 8 <= K <= BITNET_MAX_K, 1 <= V <= BITNET_MAX_N,
  * M <= BITNET_MAX_M, ceil(M/128) * ceil(V/128) <= 2^30; else

@@ -141,11 +141,18 @@ __device__ __forceinline__ void ce_join(float& mx, float& sum, float pm, float p
 }
 
 // Loss and lse of a row from the statistics of all entries but the target's.
+// A target at -inf has no weight in lse and a loss of inf; one at +inf gives
+// inf - inf.
 __device__ __forceinline__ void ce_finish(float mx, float sum, bool valid, float z, float* loss,
                                           float* lse) {
   if (!valid) {
     *loss = 0.0f;
     *lse = mx + logf(sum);
+    return;
+  }
+  if (z == -INFINITY) {
+    *lse = mx + logf(sum);
+    *loss = *lse - z;
     return;
   }
   const float d = mx - z;  // loss = log(1 + sum exp(mx - z))
@@ -154,7 +161,7 @@ __device__ __forceinline__ void ce_finish(float mx, float sum, bool valid, float
     l = z - z;  // no other entry with any weight (NaN for a non-finite z)
   else
     l = d <= 0.0f ? log1pf(sum * expf(d)) : d + logf(sum + expf(-d));
-  *loss = l;
+  *loss = z < INFINITY ? l : z - z;
   *lse = z + l;
 }
 

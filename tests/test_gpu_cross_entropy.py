@@ -338,3 +338,37 @@ def test_non_finite_upstream_gradients_stay_their_own(M, V, K, bad):
     dx, _ = tql.bitnet_cross_entropy_backward(x, W, t, lse, torch.where(keep, 0.0, bad),
                                               need_dW=False)
     assert (dx[keep] == 0).all() and not torch.isfinite(dx[~keep]).any()
+
+
+@pytest.mark.parametrize("M,V,K", [(7, 300, 64), (300, 700, 72)])
+def test_infinite_logits(M, V, K):
+    """An entry whose logit is -inf for every token has no weight: as if the
+    vocabulary ended before it; as the target its loss is inf, by the formula
+    with lse as it is, and its gradient -1.  A target at +inf gives inf - inf."""
+    x, W, t, d = _inputs(M, V, K, seed=V, ignored=False)
+    x[:, 0] = x[:, 0].abs() + 0.5
+    at = V - 1
+    t[t == at] = 0
+    exact, tol = _exact(x, W[:at], t, d)
+    Wm = W.clone()
+    Wm[at, 0] = -torch.inf
+    loss, lse = tql.bitnet_cross_entropy_forward(x, Wm, t)
+    _close({"loss": loss, "lse": lse}, exact, tol)
+    _, dW = tql.bitnet_cross_entropy_backward(x, Wm, t, lse, d, need_dx=False)
+    _close({"dW": dW[:at]}, exact, tol)
+    assert (dW[at] == 0).all()
+    t2 = t.clone()
+    t2[2] = at
+    loss, lse = tql.bitnet_cross_entropy_forward(x, Wm, t2)
+    assert loss[2] == torch.inf
+    _close({"lse": lse}, exact, tol)
+    # g of that row is dloss (softmax - onehot), the onehot at an entry of no weight
+    only = torch.zeros_like(d)
+    only[2] = 1.0
+    _, dW = tql.bitnet_cross_entropy_backward(x, Wm, t2, lse, only, need_dx=False)
+    assert torch.equal(dW[at], -x[2])
+    Wp = W.clone()
+    Wp[at, 0] = torch.inf
+    loss, lse = tql.bitnet_cross_entropy_forward(x, Wp, t2)
+    assert not torch.isfinite(lse).any() and torch.isnan(loss[2])
+    assert not torch.isfinite(loss).any()
