@@ -64,14 +64,18 @@ __device__ __forceinline__ float ce_target_dot(const __nv_bfloat16* __restrict__
 }
 
 // The statistics of a row over half a tile's columns, the target's left out.
-// On single SMs the tensor cores sum runs of 8 steps, 512 terms: 100 tokens
-// over 2000 x 4096, all terms positive, lse off by 1.4e-5 instead of 4.4e-4,
-// and one token's loss by 1e-7 of itself instead of 1e-6, in the same time
-// (48.5 us over 32000 x 4096).  CeGrad forms its logits the same way: e^(z - lse)
-// wants both off alike.
+// The tensor cores sum runs of 8 steps, 512 terms, on single SMs, and of 16 on
+// pairs, where a run has to outlast half of the epilogue (8 there: 8192 tokens
+// over 128000 x 4096 6.35 ms, 16: 6.01).  100 tokens over 2000 x 4096, all
+// terms positive: lse off by 1.4e-5 instead of 4.4e-4, and one token's loss by
+// 1e-7 of itself instead of 1e-6, in the same time (48.5 us over 32000 x 4096);
+// 256 tokens over 40000 x 4096: 4.2e-5 instead of 4.2e-4.  The loss takes the
+// target's logit from a sum of its own, so what the others lose stays in it.
+// CeGrad forms its logits in runs as short (from the other end of the
+// contraction: other roundings), since e^(z - lse) wants both off alike.
 struct CeStats {
   static constexpr bool kAMn = false, kBMn = false, kBf16 = true;
-  static constexpr int kRun = 8, kSlots = 0, kSlotBytes = 0;
+  static constexpr int kRun = 8, kPairRun = 16, kSlots = 0, kSlotBytes = 0;
   struct Params {
     const int64_t* targets;
     float2* part;          // [2 nt][M]: maximum, sum of exp(z - maximum)
@@ -84,12 +88,8 @@ struct CeStats {
                                              const TgPart& t, TgStage&, Src src) {
     const int64_t target = t.live ? __ldg(e.targets + t.row) : -1;
     float mx = -INFINITY, sum = 0.0f;
-    const int n = t.chunks();
-#pragma unroll 1
-    for (int k = 0; k < n; ++k) {
-      const int c = t.first + k * t.step, col = t.col0 + c;
-      uint32_t r[32];
-      src.load(c, r);
+    tg_chunks(t, src, [&](int k, uint32_t (&r)[32]) {
+      const int col = t.col0 + t.first + k * t.step;
       if (col + 32 > t.col_end) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -121,7 +121,7 @@ struct CeStats {
           if (__uint_as_float(r[i]) != -INFINITY) nan = __uint_as_float(r[i]);
         sum += nan;
       }
-    }
+    });
     if (t.live)
       e.part[(2 * static_cast<int64_t>(t.tile.n) + (t.first >> 5)) * p.M + t.row] =
           make_float2(mx, sum);
@@ -274,7 +274,8 @@ ce_target_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __res
 
 struct CeGrad {
   static constexpr bool kAMn = false, kBMn = false, kBf16 = true;
-  static constexpr int kRun = CeStats::kRun, kSlots = 2, kSlotBytes = 2048;
+  static constexpr int kRun = CeStats::kRun, kPairRun = CeStats::kPairRun;
+  static constexpr int kSlots = 2, kSlotBytes = 2048;
   struct Params {
     const int64_t* targets;
     const float* lse;
@@ -300,12 +301,9 @@ struct CeGrad {
       at_target = expm1f(__ldcg(e.logit + t.row) - l);
       target -= e.v0;
     }
-    const int n = t.chunks();
-#pragma unroll 1
-    for (int k = 0; k < n; ++k) {
-      const int c = t.first + k * t.step, col = t.col0 + c;
-      uint32_t r[32], w[16];
-      src.load(c, r);
+    tg_chunks(t, src, [&](int k, uint32_t (&r)[32]) {
+      const int col = t.col0 + t.first + k * t.step;
+      uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         r[i] = __float_as_uint(
@@ -327,8 +325,15 @@ struct CeGrad {
       __syncwarp();
       tg_store_block(st, &m.out, blk, col, t);
       if (st.lane == 0) bulk_commit();
-    }
+    });
   }
+};
+
+// The same on pairs whose contraction is one run: straight from TMEM (1024
+// tokens over 32000 x 512: the statistics 34 us, 40 through registers).
+template <class Epi>
+struct CeWhole : Epi {
+  static constexpr int kPairRun = 0;
 };
 
 // dx of a split contraction: add + the slices in order, in fp32, or times

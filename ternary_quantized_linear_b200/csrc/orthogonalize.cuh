@@ -285,7 +285,7 @@ __device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const 
 // where the products take it).
 struct OrthoGram {
   static constexpr bool kAMn = false, kBMn = false, kBf16 = false;
-  static constexpr int kRun = 0, kSlots = 2, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kPairRun = 0, kSlots = 2, kSlotBytes = 4096;
   struct Params {
     float* D;              // [batch][n]
     int low;               // R's low half too (then not symmetric tiles)
@@ -323,7 +323,7 @@ struct OrthoGram {
 // R R, and from it Q (fp16) and a + E (fp32, the factor of X).
 struct OrthoPoly {
   static constexpr bool kAMn = false, kBMn = false, kBf16 = false;
-  static constexpr int kRun = 0, kSlots = 3, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kPairRun = 0, kSlots = 3, kSlotBytes = 4096;
   struct Params {
     const float* D;
     float* E;              // [batch][n]: a + b D + c (D^2 + (R R)_ii)
@@ -407,7 +407,7 @@ struct OrthoPoly {
 // (transposed back for a tall update).
 struct OrthoUpdate {
   static constexpr bool kAMn = false, kBMn = true, kBf16 = false;
-  static constexpr int kRun = 0, kSlots = 3, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kPairRun = 0, kSlots = 3, kSlotBytes = 4096;
   struct Params {
     const float* E;
     __nv_bfloat16* out;    // last step: [batch][n][k], or [batch][k][n] when tall; else null

@@ -38,11 +38,14 @@
 //
 // The tensor cores truncate every sum: 16 terms at a time, half a unit of the
 // last place off toward zero on average, so a logit of 4096 terms comes out
-// some 1e-5 of itself too small.  An epilogue that needs better (kRun) has the
-// contraction in runs of so many steps on single SMs, which its warps add up
-// with rounding in the second accumulator; where few rows leave the tensor
-// cores waiting for memory that costs nothing.  Pairs have no accumulator to
-// spare, and take contractions whole.
+// some 1e-5 of itself too small.  An epilogue that needs better (kRun, kPairRun)
+// has the contraction in runs of so many steps, which its warps add up with
+// rounding: on single SMs in the second accumulator; a pair's tile fills TMEM
+// with its two, which its runs take in turn, and the sums are held in registers,
+// 128 a thread.  Terms of one sign, logits of 40, 256 tokens over 40000 entries:
+// the loss is off by 1.2e-5, 4.0e-5 and 1.2e-4 of itself for 2048, 4096 and 8192
+// terms in one go, by 3.9e-6 for each in runs of 16 steps (fp32 torch 2.7e-6,
+// 3.4e-6, 5.6e-6).
 //
 // A product of fewer than 128 rows copies only those (rounded up to 8): the
 // MMA then takes whatever follows in the ring for the missing rows, whose sums
@@ -64,6 +67,13 @@ constexpr int kTgEpiWarps = 8;
 constexpr int kTgKStep = 64;  // elements: one 128-byte swizzle row
 
 constexpr int kTgMaxStages = 16;
+
+// Registers of a thread at launch (65536 over 384 threads, a multiple of 8), and
+// after the split where the epilogue keeps sums in them: warps 0 to 3 need 40,
+// the rest goes to the epilogue (216, with 72 for the others, spills).
+constexpr int kTgRegs = 168, kTgLightRegs = 40, kTgEpiRegs = 232;
+static_assert(128 * kTgLightRegs + 32 * kTgEpiWarps * kTgEpiRegs <= kTgThreads * kTgRegs,
+              "the split may not ask for more than the block was launched with");
 
 // Epi::kSlots blocks of Epi::kSlotBytes per epilogue warp for its tensors; the
 // rest of shared memory is the ring.
@@ -227,6 +237,26 @@ __device__ __forceinline__ void tg_tmem_dealloc(uint32_t taddr, uint32_t ncols) 
                  : "memory");
   else
     tmem_dealloc(taddr, ncols);
+}
+
+// Give back registers, or take more (waits until others gave theirs back): all
+// warps of a warpgroup.
+template <int N, bool kMore>
+__device__ __forceinline__ void set_max_regs() {
+  if constexpr (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// True in one lane of the warp, the same one every time; all lanes call it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}" : "=r"(one)::"memory");
+  return one != 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -458,6 +488,7 @@ __device__ __forceinline__ uint8_t* tg_out_block(TgStage& st) {
 // Accumulator values of this thread's row, 32 columns from column c of the
 // tile: from TMEM, or the sum over the CTAs of a cluster.
 struct TgTmemSrc {
+  static constexpr bool kRegs = false;
   uint32_t addr;
   __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
     tmem_ld_32x32b_x32(addr + c, r);
@@ -465,8 +496,37 @@ struct TgTmemSrc {
   }
 };
 
+// A pair's sums of runs, in the epilogue's registers: 4 chunks of 32 columns of
+// a thread's row.  Registers have no indexes, so the chunks come to the front
+// one after another (unrolled instead, the epilogue is four times as much code
+// to arrive on its first pass, which is longer than the two runs it may take).
+struct TgRegSrc {
+  static constexpr bool kRegs = true;
+  float (&sum)[128];
+};
+
+// Calls f(k, r) for the part's chunks: r holds 32 columns from first + k * step.
+template <class Src, class F>
+__device__ __forceinline__ void tg_chunks(const TgPart& t, const Src& src, F&& f) {
+  const int n = t.chunks();
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    uint32_t r[32];
+    if constexpr (Src::kRegs) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src.sum[i]);
+#pragma unroll
+      for (int i = 0; i < 96; ++i) src.sum[i] = src.sum[i + 32];
+    } else {
+      src.load(t.first + k * t.step, r);
+    }
+    f(k, r);
+  }
+}
+
 // The last run of a contraction and the sum of those before it (none: !more).
 struct TgRunSrc {
+  static constexpr bool kRegs = false;
   uint32_t addr, sum;
   bool more;
   __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
@@ -545,9 +605,12 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int CLUSTER = CG * SPLIT;
-  // Steps that the tensor cores sum before the epilogue warps add the run up
-  // (then one accumulator holds the run, the other the sum); 0: all of them.
-  constexpr int RUN = CG == 1 && SPLIT == 1 ? Epi::kRun : 0;
+  // Steps that the tensor cores sum before the epilogue warps add the run up;
+  // 0: all of them.  On single SMs one accumulator holds the run, the other the
+  // sum; a pair's runs alternate between the two and its sums are in registers.
+  constexpr int RUN = SPLIT > 1 ? 0 : CG == 2 ? Epi::kPairRun : Epi::kRun;
+  constexpr bool kRegs = CG == 2 && RUN > 0;
+  constexpr bool kOneBuf = CG == 1 && RUN > 0;
   const uint32_t rank = CLUSTER > 1 ? cluster_rank() : 0u;
   const uint32_t half_rank = CG == 2 ? rank : 0u;  // which half of the pair's tile
   const uint64_t limit = p.wait_limit_ns;
@@ -623,197 +686,142 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
   st.pre[0] = st.pre[1] = 0.0f;
   const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0, s = 0, round = 0;  // stages issued, the ring's place
-      bool ok = true;
-      // The first tile's place is worked out before the launch before has
-      // ended (its divisions take 1500 cycles with cold instructions).
-      int t = worker;
-      TgTile tile = tg_tile(p, t);
-      int k_lo, k_hi;
-      k_range(tile.split, k_lo, k_hi);
-      pdl_wait_prior_grid();
-      pdl_launch_dependents();
-      while (true) {
-        const int a0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank);
-        const int b0 = tile.n * (CG * b_rows) + b_rows * static_cast<int>(half_rank);
-        for (int pass = 0; pass < p.passes && ok; ++pass) {
-          const CUtensorMap* ma = pass == 2 ? &maps.a_lo : &maps.a;
-          const CUtensorMap* mb = pass == 1 ? &maps.b_lo : &maps.b;
-          for (int j = k_lo; j < k_hi; ++j, ++it) {
-            if (round > 0 && !mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, limit)) {
-              *abort_flag = 1;
-              record_failure(p.status, DEV_TIMEOUT_PRODUCER);
-              ok = false;
-              break;
-            }
-            const uint32_t dst = smem_u32(smem) + s * stage_bytes;
-            uint32_t bar = smem_u32(&full[s]);
-            if (CG == 2) bar = map_to_rank(bar, 0);
-            if (half_rank == 0) mbar_arrive_expect_tx(&full[s], stage_tx);
-            const int k0 = (p.backwards ? k_hi - 1 - (j - k_lo) : j) * kTgKStep;
-            tg_load<CG, Epi::kAMn>(ma, a_rows, dst, a0, k0, tile.b, bar);
-            tg_load<CG, Epi::kBMn>(mb, b_rows, dst + a_bytes, b0, k0, tile.b, bar);
-            if (++s == stages) {
-              s = 0;
-              ++round;
-            }
-          }
-        }
-        t += workers;
-        if (t >= p.tiles || !ok) break;
-        tile = tg_tile(p, t);
-        k_range(tile.split, k_lo, k_hi);
-      }
-      // The last commits must have arrived before this CTA's barriers go away.
-      const uint32_t from = it > stages ? it - stages : 0u;
-      for (uint32_t i = from; i < it && ok; ++i)
-        if (!mbar_wait_bounded(&empty[i % stages], (i / stages) & 1u, abort_flag, limit)) {
-          *abort_flag = 1;
-          record_failure(p.status, DEV_TIMEOUT_PRODUCER);
-          ok = false;
-        }
-      // After a timeout, let the copies in flight land first (otherwise the
-      // MMAs have consumed them all).
-      if (*abort_flag && half_rank == 0)
-        for (uint32_t i = from; i < it; ++i)
-          if (!mbar_wait_bounded(&full[i % stages], (i / stages) & 1u, nullptr, limit))
-            record_failure(p.status, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && half_rank == 0) {
-      // This one thread feeds the tensor cores of the pair, a step of 512
-      // cycles: whatever it need not compute per step is outside the loop or a
-      // constant (operand layouts as run-time choices cost 8 % of the rate).
-      const uint32_t a = smem_u32(smem);
-      const uint64_t desc_a = Epi::kAMn ? umma_desc_sw128_mnmajor(a) : umma_desc_sw128_kmajor(a);
-      const uint64_t desc_b = Epi::kBMn ? umma_desc_sw128_mnmajor(a + a_bytes)
-                                        : umma_desc_sw128_kmajor(a + a_bytes);
-      const uint32_t idesc =
-          CG == 2 ? tg_idesc(256, BN, Epi::kBf16, Epi::kAMn, Epi::kBMn) : p.idesc;
-      uint32_t s = 0, ph = 0;
-      int local = 0;
-      bool ok = true;
-      for (int t = worker; t < p.tiles && ok; t += workers) {
+  if (warp < 4) {
+    if constexpr (kRegs) set_max_regs<kTgLightRegs, false>();
+    if (warp == 0) {
+      if (lane == 0) {
+        uint32_t it = 0, s = 0, round = 0;  // stages issued, the ring's place
+        bool ok = true;
+        // The first tile's place is worked out before the launch before has
+        // ended (its divisions take 1500 cycles with cold instructions).
+        int t = worker;
+        TgTile tile = tg_tile(p, t);
         int k_lo, k_hi;
-        k_range(p.ksplit > 1 ? t % p.ksplit : 0, k_lo, k_hi);
-        const int n_it = (k_hi - k_lo) * p.passes;
-        int j = 0;
-        do {
-          const int buf = RUN > 0 ? 0 : local & 1;
-          const int start = RUN > 0 ? j : 0, end = RUN > 0 ? min(n_it, j + RUN) : n_it;
-          const bool used = local >= (RUN > 0 ? 1 : 2);
-          const uint32_t before = static_cast<uint32_t>(RUN > 0 ? local - 1 : (local >> 1) - 1);
-          if (used && !mbar_wait_bounded(&accempty[buf], before & 1u, abort_flag, limit)) {
+        k_range(tile.split, k_lo, k_hi);
+        pdl_wait_prior_grid();
+        pdl_launch_dependents();
+        while (true) {
+          const int a0 = tile.m * 128 * CG + 128 * static_cast<int>(half_rank);
+          const int b0 = tile.n * (CG * b_rows) + b_rows * static_cast<int>(half_rank);
+          for (int pass = 0; pass < p.passes && ok; ++pass) {
+            const CUtensorMap* ma = pass == 2 ? &maps.a_lo : &maps.a;
+            const CUtensorMap* mb = pass == 1 ? &maps.b_lo : &maps.b;
+            for (int j = k_lo; j < k_hi; ++j, ++it) {
+              if (round > 0 && !mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, limit)) {
+                *abort_flag = 1;
+                record_failure(p.status, DEV_TIMEOUT_PRODUCER);
+                ok = false;
+                break;
+              }
+              const uint32_t dst = smem_u32(smem) + s * stage_bytes;
+              uint32_t bar = smem_u32(&full[s]);
+              if (CG == 2) bar = map_to_rank(bar, 0);
+              if (half_rank == 0) mbar_arrive_expect_tx(&full[s], stage_tx);
+              const int k0 = (p.backwards ? k_hi - 1 - (j - k_lo) : j) * kTgKStep;
+              tg_load<CG, Epi::kAMn>(ma, a_rows, dst, a0, k0, tile.b, bar);
+              tg_load<CG, Epi::kBMn>(mb, b_rows, dst + a_bytes, b0, k0, tile.b, bar);
+              if (++s == stages) {
+                s = 0;
+                ++round;
+              }
+            }
+          }
+          t += workers;
+          if (t >= p.tiles || !ok) break;
+          tile = tg_tile(p, t);
+          k_range(tile.split, k_lo, k_hi);
+        }
+        // The last commits must have arrived before this CTA's barriers go away.
+        const uint32_t from = it > stages ? it - stages : 0u;
+        for (uint32_t i = from; i < it && ok; ++i)
+          if (!mbar_wait_bounded(&empty[i % stages], (i / stages) & 1u, abort_flag, limit)) {
             *abort_flag = 1;
-            record_failure(p.status, DEV_TIMEOUT_MMA);
+            record_failure(p.status, DEV_TIMEOUT_PRODUCER);
             ok = false;
-            break;
           }
-          tc_fence_after_sync();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-          for (; j < end; ++j) {
-            if (!mbar_wait_bounded(&full[s], ph, abort_flag, limit)) {
-              *abort_flag = 1;
-              record_failure(p.status, DEV_TIMEOUT_MMA);
-              ok = false;
-              break;
-            }
+        // After a timeout, let the copies in flight land first (otherwise the
+        // MMAs have consumed them all).
+        if (*abort_flag && half_rank == 0)
+          for (uint32_t i = from; i < it; ++i)
+            if (!mbar_wait_bounded(&full[i % stages], (i / stages) & 1u, nullptr, limit))
+              record_failure(p.status, DEV_TIMEOUT_DRAIN);
+      }
+    } else if (warp == 1) {
+      if (half_rank == 0) {
+        // This warp feeds the tensor cores of the pair, a step of 512 cycles:
+        // whatever it need not compute per step is outside the loop or a constant
+        // (operand layouts as run-time choices cost 8 % of the rate), and the
+        // whole warp takes the loop, one lane of it issuing, so that addresses are
+        // uniform values.  With one lane in the loop a run's end cost some 1000
+        // cycles: 8192 tokens over 128000 x 4096 in runs of 16 steps 6.51 ms, so 6.01.
+        const uint32_t a = smem_u32(smem);
+        const uint64_t desc_a = Epi::kAMn ? umma_desc_sw128_mnmajor(a) : umma_desc_sw128_kmajor(a);
+        const uint64_t desc_b = Epi::kBMn ? umma_desc_sw128_mnmajor(a + a_bytes)
+                                          : umma_desc_sw128_kmajor(a + a_bytes);
+        const uint32_t idesc =
+            CG == 2 ? tg_idesc(256, BN, Epi::kBf16, Epi::kAMn, Epi::kBMn) : p.idesc;
+        // (one answer for all lanes: they go on, or stop, together)
+        auto there = [&](uint64_t* bar, uint32_t parity) {
+          if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, limit)))
+            return true;
+          *abort_flag = 1;
+          if (lane == 0) record_failure(p.status, DEV_TIMEOUT_MMA);
+          return false;
+        };
+        uint32_t s = 0, ph = 0;
+        int local = 0;
+        bool ok = true;
+        for (int t = worker; t < p.tiles && ok; t += workers) {
+          int k_lo, k_hi;
+          k_range(p.ksplit > 1 ? t % p.ksplit : 0, k_lo, k_hi);
+          const int n_it = (k_hi - k_lo) * p.passes;
+          int j = 0;
+          do {
+            const int buf = kOneBuf ? 0 : local & 1;
+            const int start = RUN > 0 ? j : 0, end = RUN > 0 ? min(n_it, j + RUN) : n_it;
+            const bool used = local >= (kOneBuf ? 1 : 2);
+            const uint32_t before = static_cast<uint32_t>(kOneBuf ? local - 1 : (local >> 1) - 1);
+            ok = !used || there(&accempty[buf], before & 1u);
+            if (!ok) break;
             tc_fence_after_sync();
-            // (start addresses stay below 2^18: adding to the field is safe)
-            const uint64_t at = s * (stage_bytes >> 4);
+            const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+            for (; j < end; ++j) {
+              ok = there(&full[s], ph);
+              if (!ok) break;
+              tc_fence_after_sync();
+              // (start addresses stay below 2^18: adding to the field is safe)
+              const uint64_t at = s * (stage_bytes >> 4);
+              if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTgKStep / 16; ++kk)
-              tg_mma<CG>(d, desc_a + at + (Epi::kAMn ? 128 : 2) * kk,
-                         desc_b + at + (Epi::kBMn ? 128 : 2) * kk, idesc,
-                         (kk > 0 || j > start) ? 1u : 0u);
-            tg_commit<CG>(&empty[s]);
-            if (++s == stages) {
-              s = 0;
-              ph ^= 1u;
+                for (int kk = 0; kk < kTgKStep / 16; ++kk)
+                  tg_mma<CG>(d, desc_a + at + (Epi::kAMn ? 128 : 2) * kk,
+                             desc_b + at + (Epi::kBMn ? 128 : 2) * kk, idesc,
+                             (kk > 0 || j > start) ? 1u : 0u);
+                tg_commit<CG>(&empty[s]);
+              }
+              __syncwarp();
+              if (++s == stages) {
+                s = 0;
+                ph ^= 1u;
+              }
             }
-          }
-          if (ok) tg_commit<CG>(&accfull[buf]);
-          ++local;
-        } while (RUN > 0 && ok && j < n_it);
-      }
-      if (*abort_flag) {  // the MMAs issued so far still read shared memory
-        tg_commit<CG>(drain);
-        if (!mbar_wait_bounded(drain, 0u, nullptr, limit))
-          record_failure(p.status, DEV_TIMEOUT_DRAIN);
-      }
-    }
-  } else if (warp >= 4) {
-    {
-      TgPart t = part_of(TgTile{0, 0, 0, 0}, q, half);
-      t.dry = true;
-      t.live = t.any = false;
-      t.first = 0;
-      t.col_end = min(t.col_end, 32);
-      if constexpr (SPLIT == 1) {
-        if constexpr (RUN > 0)
-          Epi::run(ep, p, maps, t, st, TgRunSrc{lanes, lanes + BN, false});
-        else
-          Epi::run(ep, p, maps, t, st, TgTmemSrc{lanes});
-      } else {
-        Epi::run(ep, p, maps, t, st,
-                 TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem)});
-      }
-      st.seq = 0;
-    }
-    TgPart part = part_of(tg_tile(p, worker), q, half);
-    pdl_wait_prior_grid();
-    int local = 0;
-    for (int t = worker; t < p.tiles; ++local) {
-      const int buf = RUN > 0 ? 0 : local & 1;
-      if constexpr (SPLIT == 1) Epi::begin(st, maps, ep, p, part);
-      auto summed = [&]() {
-        const int turn = RUN > 0 ? local : local >> 1;
-        return __all_sync(0xFFFFFFFFu,
-                          mbar_wait_bounded(&accfull[buf], static_cast<uint32_t>(turn) & 1u,
-                                            abort_flag, limit));
-      };
-      bool ok = true, more = false;
-      if constexpr (RUN > 0) {
-        for (int j = RUN; j < p.steps && ok; j += RUN) {  // all runs but the last
-          ok = summed();
-          if (!ok) break;
-          tc_fence_after_sync();
-          TgRunSrc{lanes, lanes + BN, more}.add(part);
-          more = true;
-          tc_fence_before_sync();
+            if (ok && elect_one()) tg_commit<CG>(&accfull[buf]);
+            __syncwarp();
+            ++local;
+          } while (RUN > 0 && ok && j < n_it);
+        }
+        if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) {
+          // The MMAs issued so far still read shared memory.
+          if (elect_one()) tg_commit<CG>(drain);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&accempty[0]);
-          ++local;
+          if (!mbar_wait_bounded(drain, 0u, nullptr, limit) && lane == 0)
+            record_failure(p.status, DEV_TIMEOUT_DRAIN);
         }
       }
-      ok = ok && summed();
-      if (!ok) {
-        *abort_flag = 1;
-        if (lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
-        if constexpr (SPLIT == 1) Epi::abandon(st, ep, part);
-        break;
-      }
-      tc_fence_after_sync();
-      const uint32_t acc = lanes + static_cast<uint32_t>(buf * BN);
-      if constexpr (SPLIT == 1) {
-        if constexpr (RUN > 0)
-          Epi::run(ep, p, maps, part, st, TgRunSrc{acc, acc + BN, more});
-        else
-          Epi::run(ep, p, maps, part, st, TgTmemSrc{acc});
-      } else {
-        // This CTA's part, [column][row] fp32, over the ring (all consumed).
-        float* part_sum = reinterpret_cast<float*>(smem);
-#pragma unroll 1
-        for (int c = 32 * half; c < BN; c += 64) {
-          uint32_t r[32];
-          TgTmemSrc{acc}.load(c, r);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            part_sum[(c + i) * 128 + 32 * q + lane] = __uint_as_float(r[i]);
-        }
-      }
+    }
+  } else {
+    // This warp has read accumulator `buf`.
+    auto release = [&](int buf) {
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -822,8 +830,117 @@ tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
         else
           mbar_arrive(&accempty[buf]);
       }
-      t += workers;
-      if (t < p.tiles) part = part_of(tg_tile(p, t), q, half);
+    };
+    // The next turn of accumulator `buf` has its sums.
+    auto summed = [&](int buf, int turn) {
+      return __all_sync(0xFFFFFFFFu,
+                        mbar_wait_bounded(&accfull[buf], static_cast<uint32_t>(turn) & 1u,
+                                          abort_flag, limit));
+    };
+    auto give_up = [&](const TgPart& part) {
+      *abort_flag = 1;
+      if (lane == 0) record_failure(p.status, DEV_TIMEOUT_EPILOGUE);
+      if constexpr (SPLIT == 1) Epi::abandon(st, ep, part);
+    };
+    TgPart part = part_of(TgTile{0, 0, 0, 0}, q, half);
+    part.dry = true;
+    part.live = part.any = false;
+    part.first = 0;
+    part.col_end = min(part.col_end, 32);
+    if constexpr (kRegs) {
+      set_max_regs<kTgEpiRegs, true>();
+      int local = 0;
+      for (int t = worker; t < p.tiles;) {
+        float sum[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
+        bool ok = true;
+        if (!part.dry) {
+          Epi::begin(st, maps, ep, p, part);
+#pragma unroll 1
+          for (int j = 0; j < p.steps; j += RUN, ++local) {
+            const int buf = local & 1;
+            ok = summed(buf, local >> 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t r[32];
+              TgTmemSrc{lanes + static_cast<uint32_t>(buf * BN + 32 * half)}.load(64 * k, r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sum[32 * k + i] = __fadd_rn(sum[32 * k + i], __uint_as_float(r[i]));
+            }
+            release(buf);
+          }
+        }
+        if (!ok) {
+          give_up(part);
+          break;
+        }
+        Epi::run(ep, p, maps, part, st, TgRegSrc{sum});
+        const bool dry = part.dry;
+        if (!dry) t += workers;
+        if (t < p.tiles) part = part_of(tg_tile(p, t), q, half);
+        if (dry) {
+          st.seq = 0;
+          pdl_wait_prior_grid();
+        }
+      }
+    } else {
+      if constexpr (SPLIT > 1)
+        Epi::run(ep, p, maps, part, st, TgClusterSrc<SPLIT>{reinterpret_cast<const float*>(smem)});
+      else if constexpr (kOneBuf)
+        Epi::run(ep, p, maps, part, st, TgRunSrc{lanes, lanes + BN, false});
+      else
+        Epi::run(ep, p, maps, part, st, TgTmemSrc{lanes});
+      st.seq = 0;
+      part = part_of(tg_tile(p, worker), q, half);
+      pdl_wait_prior_grid();
+      int local = 0;
+      for (int t = worker; t < p.tiles; ++local) {
+        const int buf = kOneBuf ? 0 : local & 1;
+        if constexpr (SPLIT == 1) Epi::begin(st, maps, ep, p, part);
+        bool ok = true, more = false;
+        if constexpr (kOneBuf) {
+          for (int j = RUN; j < p.steps && ok; j += RUN) {  // all runs but the last
+            ok = summed(0, local);
+            if (!ok) break;
+            tc_fence_after_sync();
+            TgRunSrc{lanes, lanes + BN, more}.add(part);
+            more = true;
+            release(0);
+            ++local;
+          }
+        }
+        ok = ok && summed(buf, kOneBuf ? local : local >> 1);
+        if (!ok) {
+          give_up(part);
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t acc = lanes + static_cast<uint32_t>(buf * BN);
+        if constexpr (SPLIT == 1) {
+          if constexpr (kOneBuf)
+            Epi::run(ep, p, maps, part, st, TgRunSrc{acc, acc + BN, more});
+          else
+            Epi::run(ep, p, maps, part, st, TgTmemSrc{acc});
+        } else {
+          // This CTA's part, [column][row] fp32, over the ring (all consumed).
+          float* part_sum = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+          for (int c = 32 * half; c < BN; c += 64) {
+            uint32_t r[32];
+            TgTmemSrc{acc}.load(c, r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              part_sum[(c + i) * 128 + 32 * q + lane] = __uint_as_float(r[i]);
+          }
+        }
+        release(buf);
+        t += workers;
+        if (t < p.tiles) part = part_of(tg_tile(p, t), q, half);
+      }
     }
   }
   __syncwarp();
@@ -892,7 +1009,7 @@ __device__ __forceinline__ void tg_store_block(const TgStage& st, const CUtensor
 // 32000 x 2048 at 2.9 TB/s; a plain fill of that size reaches 3.5).
 struct TgStoreBf16 {
   static constexpr bool kAMn = true, kBMn = true, kBf16 = true;
-  static constexpr int kRun = 0, kSlots = 2, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kPairRun = 0, kSlots = 2, kSlotBytes = 4096;
   struct Params {
     const float* scale;
   };
@@ -931,7 +1048,7 @@ struct TgStoreBf16 {
 // a split contraction goes to its own [M][N] of the output.
 struct TgAccumulate {
   static constexpr bool kAMn = false, kBMn = true, kBf16 = true;
-  static constexpr int kRun = 0, kSlots = 3, kSlotBytes = 4096;
+  static constexpr int kRun = 0, kPairRun = 0, kSlots = 3, kSlotBytes = 4096;
   struct Params {
     int add;             // add `in`
     int to_bf16;         // `out` is bf16 (else fp32)

@@ -149,6 +149,11 @@ int tg_workers(int num_sms) {
     using C = TgCfg<CG, BN, Epi>;
     auto kernel = tc_gemm_kernel<CG, BN, SPLIT, Epi>;
     if (!set_smem(kernel, C::SMEM_DYN)) return;
+    // (a split of registers that the launch does not have would wait for good)
+    cudaFuncAttributes attr_of{};
+    if (CG == 2 && Epi::kPairRun > 0 &&
+        (cudaFuncGetAttributes(&attr_of, kernel) != cudaSuccess || attr_of.numRegs < kTgRegs))
+      return;
     if (CG == 1) {
       workers[dev] = num_sms;
       return;
@@ -273,6 +278,15 @@ bitnet_status launch_tg(const DeviceState& ds, const TgProblem& g,
                         TgReady* ready = nullptr) {
   return g.plan.cg == 2 ? launch_tg_cfg<2, 256, 1, Epi>(ds, g, ep, stream, ready)
                         : launch_tg_cfg<1, BN1, 1, Epi>(ds, g, ep, stream, ready);
+}
+
+// A head's logits: pairs sum contractions of more than one run in runs.
+template <class Epi>
+bitnet_status launch_logits(const DeviceState& ds, const TgProblem& g,
+                            const typename Epi::Params& ep, cudaStream_t stream) {
+  if (g.plan.cg == 2 && ceil_div(g.Kc, kTgKStep) <= Epi::kPairRun)
+    return launch_tg_cfg<2, 256, 1, CeWhole<Epi>>(ds, g, ep, stream, nullptr);
+  return launch_tg<256, Epi>(ds, g, ep, stream);
 }
 
 // The same with the contraction of a 128 x 128 tile shared by a cluster.
@@ -610,7 +624,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_forward(const void* x, const void*
   g.Kc = K;
   g.plan = L.plan;
   CeStats::Params ep{targets, reinterpret_cast<float2*>(ws + L.part)};
-  st = launch_tg<256, CeStats>(*ds, g, ep, s);
+  st = launch_logits<CeStats>(*ds, g, ep, s);
   if (st != BITNET_OK) return st;
   // (256 rows: a block per row is two waves of them, and the wide cut's
   // neighbouring parts begin to count)
@@ -680,7 +694,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       // 32000 x 2048, loss and gradient: 149 us from the front, 143 from the end).
       g.backwards = true;
       CeGrad::Params ep{targets, lse, dloss, logit, scale, V, v0};
-      st = launch_tg<256, CeGrad>(*ds, g, ep, s);
+      st = launch_logits<CeGrad>(*ds, g, ep, s);
       if (st != BITNET_OK) return st;
     }
     if (dx) {  // dx (+)= g W_i

@@ -372,3 +372,30 @@ def test_infinite_logits(M, V, K):
     loss, lse = tql.bitnet_cross_entropy_forward(x, Wp, t2)
     assert not torch.isfinite(lse).any() and torch.isnan(loss[2])
     assert not torch.isfinite(loss).any()
+
+
+@pytest.mark.parametrize("M,V,K", [(129, 40000, 4096), (300, 20000, 4096), (1000, 9000, 2184)])
+def test_many_rows_sum_in_short_runs(M, V, K):
+    """As test_few_rows_sum_in_short_runs, on SM pairs: terms of one sign, of
+    which the tensor cores sum 1024 at a time: 64 truncations, 32.5 * 2^-23 of
+    the run together, and a rounding where it joins the others.  The loss, log(1 + sum e^(z_v - z_t)),
+    takes z_t from a sum of K/32 rounded terms in a lane and the join of the
+    lanes: partial sums of one sign grow evenly, so half of the roundings count."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (0.5 + torch.rand((M, K), generator=g, device="cuda")).bfloat16()
+    W = (0.005 + 0.01 * torch.rand((V, K), generator=g, device="cuda")).bfloat16()
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    loss, lse = (v.double() for v in tql.bitnet_cross_entropy_forward(x, W, t))
+    z = x.double() @ W.double().T
+    top = z.amax(1)
+    exact = torch.logsumexp(z, 1)
+    runs = -(-K // 1024)
+    e = (top * (32.5 * 2.0 ** -23 + (runs - 1) * 2.0 ** -24) + 2.0 ** -22 * (1 + top)
+         + 200 * 2.0 ** -24)
+    target = top * (0.55 * K / 32 + 5) * 2.0 ** -24
+    share = torch.exp(top - exact)
+    assert ((lse - exact).abs() <= e + share * target + 2.0 ** -23 * exact).all(), \
+        ((lse - exact).abs() / e).max()
+    want = exact - z[torch.arange(M, device="cuda"), t]
+    assert ((loss - want).abs() <= e + target + 2.0 ** -22 * want).all(), \
+        ((loss - want).abs() / e).max()
