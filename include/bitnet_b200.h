@@ -530,12 +530,14 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void *x, const void
  *   U            [B][N][K] fp32 or bf16 (u_dtype): B matrices, each on its own.
  *   coefficients host array of 3 * steps doubles: a, b, c of each step.
  *   O            [B][N][K] bf16 out; must not overlap U.
- *   X is held in 22 bits, A's and b A + c A A's diagonals in fp32, sums in
- *   fp32; the products' operands are fp16, for min(N, K) <= 192 in both
- *   halves (22 bits).  A non-finite entry makes its matrix NaN, a zero matrix
- *   gives zeros (eps 0 included).
+ *   X is held in 22 bits of the largest singular value that the step before can
+ *   leave (1 at first: an update far below eps keeps fewer of its own), A's and
+ *   b A + c A A's diagonals in fp32, sums in fp32; the products' operands are
+ *   fp16, for min(N, K) <= 192 in both halves (22 bits).  A non-finite entry
+ *   makes its matrix NaN, a zero matrix gives zeros (eps 0 included).
  * 1 <= steps <= 32, eps >= 0; the coefficients finite and such that no step
- * takes singular values of at most 1 beyond 2^20 (BITNET_ERR_INVALID_ARG).
+ * takes singular values of at most 1, nor its b A + c A A, beyond 2^20
+ * (BITNET_ERR_INVALID_ARG).
  * Shapes: 1 <= N, K <= BITNET_MAX_K, 0 <= B <= 65535, at most 2^30 tiles of
  * 128 x 128 in all.  U, O 16-byte aligned; workspace >= the size query (0,
  * and NULL allowed, for updates of up to 128 x 2048 or 2048 x 128), 256-byte

@@ -23,7 +23,10 @@
 //
 // fp16 has too little range for entries near 1 / n, so X, R and Q are stored
 // times powers of two that the host takes from the largest singular value
-// that each step can reach.
+// that each step can reach (D as R is, E as the factor from one stored X to the
+// next).  The powers and the coefficients meet on the host, in fp64, so that
+// iterates may shrink or grow as they like: what the kernels multiply by
+// stays near 1.
 #pragma once
 
 #include "tc_gemm.cuh"
@@ -281,6 +284,14 @@ __device__ __forceinline__ void ortho_store(TgStage& st, const TgMaps& m, const 
   if (st.lane == 0) bulk_commit();
 }
 
+// The factors of one step, between values as they are stored.
+struct OrthoStep {
+  float to_R;            // X X^T's accumulator -> R and D
+  float kr, kb;          // R R's accumulator, and D R -> Q; R -> Q
+  float ea, eb, ec;      // a + E from 1, D, and D^2 + (R R)_ii
+  float ku;              // Q X's accumulator -> X
+};
+
 // A = X X^T: its diagonal to D (fp32), the rest to R (fp16, and its low half
 // where the products take it).
 struct OrthoGram {
@@ -289,7 +300,7 @@ struct OrthoGram {
   struct Params {
     float* D;              // [batch][n]
     int low;               // R's low half too (then not symmetric tiles)
-    float to_true, to_R;   // accumulator -> A, accumulator -> stored R
+    OrthoStep f;
   };
   static __device__ __forceinline__ void begin(TgStage&, const TgMaps&, const Params&,
                                                const TgShape&, const TgPart&) {}
@@ -306,12 +317,12 @@ struct OrthoGram {
       src.load(c, r);
       float v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * e.to_R;
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * e.f.to_R;
       if (t.row0 < col + 32 && col < t.row0 + 32) {  // the diagonal passes this chunk
         const int at = t.row - col;
         const float d = chunk_pick(r, at);
         if (t.live && at >= 0 && at < 32)
-          e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.to_true;
+          e.D[static_cast<int64_t>(t.tile.b) * p.M + t.row] = d * e.f.to_R;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = i == at ? 0.0f : v[i];
       }
@@ -328,8 +339,7 @@ struct OrthoPoly {
     const float* D;
     float* E;              // [batch][n]: a + b D + c (D^2 + (R R)_ii)
     int low;               // R and Q with their low halves (then not symmetric tiles)
-    float a, b, c;
-    float acc_true, r_true, to_Q;
+    OrthoStep f;
   };
   using In = TgInput<OrthoPoly>;
   // D of this thread's row, and of the lane's column of the first chunk.
@@ -351,10 +361,8 @@ struct OrthoPoly {
     const float* D = e.D + static_cast<int64_t>(t.tile.b) * p.M;
     const float di = st.pre[0];
     float dl_next = st.pre[1];
-    // to_Q (c R R + (b + c (D_i + D_j)) R), from the accumulator and stored R
-    const float kr = e.c * e.acc_true * e.to_Q;
-    const float kd = e.c * e.r_true * e.to_Q;
-    const float ki = __fmaf_rn(e.c, di, e.b) * e.r_true * e.to_Q;
+    // Q = c R R + (b + c (D_i + D_j)) R
+    const float kr = e.f.kr, ki = __fmaf_rn(kr, di, e.f.kb);
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
@@ -385,14 +393,14 @@ struct OrthoPoly {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float dj = __shfl_sync(0xFFFFFFFFu, dl, i);
-        v[i] = __fmaf_rn(__fmaf_rn(kd, dj, ki), v[i], __uint_as_float(r[i]) * kr);
+        v[i] = __fmaf_rn(__fmaf_rn(kr, dj, ki), v[i], __uint_as_float(r[i]) * kr);
       }
       if (t.row0 < col + 32 && col < t.row0 + 32) {  // the diagonal passes this chunk
         const int at = t.row - col;
-        const float rr = chunk_pick(r, at) * e.acc_true;
+        const float rr = chunk_pick(r, at);
         if (t.live && at >= 0 && at < 32)
           e.E[static_cast<int64_t>(t.tile.b) * p.M + t.row] =
-              e.a + __fmaf_rn(e.c, __fmaf_rn(di, di, rr), e.b * di);
+              e.f.ea + __fmaf_rn(e.f.ec, __fmaf_rn(di, di, rr), e.f.eb * di);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = i == at ? 0.0f : v[i];
       }
@@ -413,7 +421,7 @@ struct OrthoUpdate {
     __nv_bfloat16* out;    // last step: [batch][n][k], or [batch][k][n] when tall; else null
     int tall;
     int direct;            // store the result without `maps.out` (rows of odd length)
-    float acc_true, x_true, to_Y;
+    float ku;              // accumulator -> the next X, or the result
   };
   using In = TgInput<OrthoUpdate>;
   static __device__ __forceinline__ void begin(TgStage& st, const TgMaps& m, const Params& e,
@@ -427,8 +435,7 @@ struct OrthoUpdate {
   template <class Src>
   static __device__ __forceinline__ void run(const Params& e, const TgShape& p, const TgMaps& m,
                                              const TgPart& t, TgStage& st, Src src) {
-    const float to = e.out ? 1.0f : e.to_Y;
-    const float ei = st.pre[0] * e.x_true * to, ku = e.acc_true * to;
+    const float ei = st.pre[0], ku = e.ku;
     const int n = t.chunks();
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
@@ -499,13 +506,6 @@ constexpr int kOsThreads = 512;
 constexpr int kOsMaxKs = 256;
 constexpr int kOsMaxCluster = 16;
 
-struct OsStep {
-  float a, b, c;
-  float gram_true, gram_R;       // accumulator -> A, accumulator -> stored R
-  float poly_true, r_true, to_Q;
-  float upd_true, x_true, to_Y;
-};
-
 struct OsParams {
   const void* U;
   __nv_bfloat16* out;
@@ -513,7 +513,7 @@ struct OsParams {
   float eps, scale;              // of the first X
   int* status;
   uint64_t wait_limit_ns;
-  OsStep step[32];
+  OrthoStep step[32];
 };
 
 struct OsSmem {
@@ -738,7 +738,7 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
   const uint32_t upd_desc = tg_idesc(128, p.ks, false, false, true);
 
   for (int it = 0; it < p.steps; ++it) {
-    const OsStep& c = p.step[it];
+    const OrthoStep& c = p.step[it];
     // A = X X^T, this CTA's columns of X
     if (tid == 0) issue(kGramCol, Xh, Xl, Xh, Xl, p.ks / 16, false, sq_desc);
     wait_mma();
@@ -750,11 +750,11 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
         tmem_ld_32x32b_x16(lanes + kGramCol + j, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) * c.gram_R;
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) * c.to_R;
         os_write16(Rh, Rl, row, j, v);
         const float d = os_pick(r, row - j);
         if (row >= j && row < j + 16) {  // the diagonal
-          D[row] = d * c.gram_true;
+          D[row] = d * c.to_R;
           *reinterpret_cast<uint16_t*>(Rh + os_at(row, row)) = 0;
           *reinterpret_cast<uint16_t*>(Rl + os_at(row, row)) = 0;
         }
@@ -817,12 +817,12 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
         if (i < mine) {
           const int col = static_cast<int>(rank) * share + first + i;
           uint16_t h, l;
-          split_half(col == row ? 0.0f : sum[i] * c.gram_R, h, l);
+          split_half(col == row ? 0.0f : sum[i] * c.to_R, h, l);
           // R is symmetric: (col, row), so that lanes are neighbours
           const int at = os_at(col, row);
           *reinterpret_cast<uint16_t*>(Rh + at) = h;
           *reinterpret_cast<uint16_t*>(Rl + at) = l;
-          if (col == row) D[row] = sum[i] * c.gram_true;
+          if (col == row) D[row] = sum[i] * c.to_R;
         }
       os_sync(false);
       if (tid < p.cluster && tid != static_cast<int>(rank)) {
@@ -845,9 +845,7 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
     // R R, and Q and a + E in its place
     if (tid == 0) issue(kPolyCol, Rh, Rl, Rh, Rl, 8, false, sq_desc);
     const float di = D[row];
-    const float kr = c.c * c.poly_true * c.to_Q;
-    const float kd = c.c * c.r_true * c.to_Q;
-    const float ki = __fmaf_rn(c.c, di, c.b) * c.r_true * c.to_Q;
+    const float kr = c.kr, ki = __fmaf_rn(kr, di, c.kb);
     wait_mma();
 #pragma unroll 1
     for (int j = 32 * grp; j < 32 * grp + 32; j += 16) {
@@ -861,14 +859,14 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
         const float4 d4 = *reinterpret_cast<const float4*>(D + j + i);
         const float dj[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
-        for (int h = 0; h < 4; ++h)  // to_Q (c R R + (b + c (D_i + D_j)) R)
-          v[i + h] = __fmaf_rn(__fmaf_rn(kd, dj[h], ki), v[i + h],
+        for (int h = 0; h < 4; ++h)  // Q = c R R + (b + c (D_i + D_j)) R
+          v[i + h] = __fmaf_rn(__fmaf_rn(kr, dj[h], ki), v[i + h],
                                __uint_as_float(r[i + h]) * kr);
       }
       os_write16(Rh, Rl, row, j, v);
-      const float rr = os_pick(r, row - j) * c.poly_true;
+      const float rr = os_pick(r, row - j);
       if (row >= j && row < j + 16) {  // the diagonal
-        E[row] = c.a + __fmaf_rn(c.c, __fmaf_rn(di, di, rr), c.b * di);
+        E[row] = c.ea + __fmaf_rn(c.ec, __fmaf_rn(di, di, rr), c.eb * di);
         *reinterpret_cast<uint16_t*>(Rh + os_at(row, row)) = 0;
         *reinterpret_cast<uint16_t*>(Rl + os_at(row, row)) = 0;
       }
@@ -877,8 +875,7 @@ ortho_small_kernel(const __grid_constant__ OsParams p) {
     // X <- E X + Q X
     if (tid == 0) issue(kUpdCol, Rh, Rl, Xh, Xl, 8, true, upd_desc);
     const bool last = it == p.steps - 1;
-    const float to = last ? 1.0f : c.to_Y;
-    const float ei = E[row] * c.x_true * to, ku = c.upd_true * to;
+    const float ei = E[row], ku = c.ku;
     wait_mma();
     const int quarter = p.ks / 4;
 #pragma unroll 1

@@ -517,10 +517,23 @@ void ortho_bounds(double a, double b, double c, double top, double* next, double
 
 // The power of two that brings values up to `top` below 2^15 (fp16 ends at
 // 65504; the slack covers the rounding that pushes a value past its bound).
-double fp16_scale(double top) {
-  if (!(top > 0.0)) top = 1.0;
-  const int e = 14 - static_cast<int>(std::ceil(std::log2(top)));
-  return std::ldexp(1.0, std::max(-40, std::min(40, e)));
+int fp16_exponent(double top) {
+  return top > 0.0 ? 14 - static_cast<int>(std::ceil(std::log2(top))) : 14;
+}
+
+// The factors of a step with coefficients c[3], and in *ex the exponent of the
+// stored X: before the step's, then the next one's (0, the result, at the last).
+// top, next: bounds of X before and after the step; poly: of b A + c A A.
+OrthoStep ortho_step(const double* c, double top, double next, double poly, bool last, int* ex) {
+  const int ey = last ? 0 : fp16_exponent(next), er = fp16_exponent(top * top);
+  const int e = ey - *ex;
+  const int eq = poly > 0.0 ? fp16_exponent(poly) : e;  // (no Q: any will do)
+  auto times = [](double v, int power) { return static_cast<float>(std::ldexp(v, power)); };
+  const OrthoStep f{times(1.0, er - 2 * *ex), times(c[2], eq - 2 * er), times(c[1], eq - er),
+                    times(c[0], e),           times(c[1], e - er),      times(c[2], e - 2 * er),
+                    times(1.0, e - eq)};
+  *ex = ey;
+  return f;
 }
 
 bitnet_status launch_ortho_small(const DeviceState& ds, const void* U, int u_bf16, int64_t B,
@@ -553,20 +566,10 @@ bitnet_status launch_ortho_small(const DeviceState& ds, const void* U, int u_bf1
   p.eps = eps;
   p.status = ds.status;
   p.wait_limit_ns = kWaitLimitNs;
-  double sx = fp16_scale(top[0]);
-  p.scale = static_cast<float>(sx);
-  for (int i = 0; i < steps; ++i) {
-    const double* c = coefficients + 3 * i;
-    const double sr = fp16_scale(top[i] * top[i]), sq = fp16_scale(poly[i]);
-    const double sy = fp16_scale(top[i + 1]);
-    p.step[i] = OsStep{static_cast<float>(c[0]),          static_cast<float>(c[1]),
-                       static_cast<float>(c[2]),          static_cast<float>(1.0 / (sx * sx)),
-                       static_cast<float>(sr / (sx * sx)), static_cast<float>(1.0 / (sr * sr)),
-                       static_cast<float>(1.0 / sr),      static_cast<float>(sq),
-                       static_cast<float>(1.0 / (sq * sx)), static_cast<float>(1.0 / sx),
-                       static_cast<float>(sy)};
-    sx = sy;
-  }
+  int ex = fp16_exponent(top[0]);
+  p.scale = std::ldexp(1.0f, ex);
+  for (int i = 0; i < steps; ++i)
+    p.step[i] = ortho_step(coefficients + 3 * i, top[i], top[i + 1], poly[i], i == steps - 1, &ex);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(B * p.cluster));
   cfg.blockDim = dim3(kOsThreads);
@@ -818,18 +821,19 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
                   dim3(static_cast<unsigned>(L.parts), static_cast<unsigned>(B)),
                   kOrthoNormThreads, s, U, u_bf16, N * K, N * K % 8 == 0 ? 1 : 0, norm);
   if (st != BITNET_OK) return st;
-  double sx = fp16_scale(top[0]);
+  int ex = fp16_exponent(top[0]);
+  const float scale = std::ldexp(1.0f, ex);
   if (tall) {
     st = launch_pdl(ortho_start_tall_kernel,
                     dim3(static_cast<unsigned>(ceil_div(N, 64)),
                          static_cast<unsigned>(ceil_div(K, 32)), static_cast<unsigned>(B)),
                     256, s, U, u_bf16, static_cast<int>(N), static_cast<int>(K), norm, L.parts,
-                    eps, static_cast<float>(sx), half_at(L.X[0]), half_at(L.X_lo[0]), L.ldx);
+                    eps, scale, half_at(L.X[0]), half_at(L.X_lo[0]), L.ldx);
   } else {
     const int64_t blocks = std::min<int64_t>(N, std::max<int64_t>(1, 16LL * ds->num_sms / B));
     st = launch_pdl(ortho_start_kernel,
                     dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(B)), 256, s, U,
-                    u_bf16, N, K, K % 8 == 0 ? 1 : 0, norm, L.parts, eps, static_cast<float>(sx),
+                    u_bf16, N, K, K % 8 == 0 ? 1 : 0, norm, L.parts, eps, scale,
                     half_at(L.X[0]), half_at(L.X_lo[0]), L.ldx);
   }
   if (st != BITNET_OK) return st;
@@ -843,10 +847,10 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
   const bool direct = !tall && L.k % 8 != 0;
   TgReady gram_ready[2], poly_ready, update_ready[2], last_ready;
   for (int i = 0; i < steps; ++i) {
-    const double* c = coefficients + 3 * i;
     const int from = i & 1, to = from ^ 1;
-    const double sr = fp16_scale(top[i] * top[i]), sq = fp16_scale(poly[i]);
-    const double sy = fp16_scale(top[i + 1]);
+    const bool last = i == steps - 1;
+    const OrthoStep f =
+        ortho_step(coefficients + 3 * i, top[i], top[i + 1], poly[i], last, &ex);
     TgProblem g;
     g.batch = B;
     g.passes = passes;
@@ -866,8 +870,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.out.batch = B;
     g.out.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     g.plan = gram_plan;
-    OrthoGram::Params gram{D, L.split ? 1 : 0, static_cast<float>(1.0 / (sx * sx)),
-                           static_cast<float>(sr / (sx * sx))};
+    OrthoGram::Params gram{D, L.split ? 1 : 0, f};
     st = launch_tg_split<OrthoGram>(*ds, g, gram, s, &gram_ready[from]);
     if (st != BITNET_OK) return st;
     // R R -> Q, E
@@ -881,10 +884,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.out.p = half_at(L.Q);
     g.out.lo = Q_lo;
     g.plan = poly_plan;
-    OrthoPoly::Params poly_p{D, E, L.split ? 1 : 0, static_cast<float>(c[0]),
-                             static_cast<float>(c[1]), static_cast<float>(c[2]),
-                             static_cast<float>(1.0 / (sr * sr)), static_cast<float>(1.0 / sr),
-                             static_cast<float>(sq)};
+    OrthoPoly::Params poly_p{D, E, L.split ? 1 : 0, f};
     st = launch_tg_split<OrthoPoly>(*ds, g, poly_p, s, &poly_ready);
     if (st != BITNET_OK) return st;
     // X <- E X + Q X
@@ -900,7 +900,6 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.in.lo = g.b.lo;
     g.in.ld = L.ldx;
     g.in.batch_stride = xb;
-    const bool last = i == steps - 1;
     g.out = g.in;
     g.out.p = half_at(L.X[to]);
     g.out.lo = half_at(L.X_lo[to]);
@@ -915,11 +914,9 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     }
     g.plan = update_plan;
     OrthoUpdate::Params up{E, last ? static_cast<__nv_bfloat16*>(O) : nullptr, tall ? 1 : 0,
-                           direct ? 1 : 0, static_cast<float>(1.0 / (sq * sx)),
-                           static_cast<float>(1.0 / sx), static_cast<float>(sy)};
+                           direct ? 1 : 0, f.ku};
     st = launch_tg_split<OrthoUpdate>(*ds, g, up, s, last ? &last_ready : &update_ready[from]);
     if (st != BITNET_OK) return st;
-    sx = sy;
   }
   return BITNET_OK;
 }

@@ -273,3 +273,34 @@ def test_every_cluster_of_small_updates(B, N, K):
     got = tql.bitnet_orthogonalize(U)
     for u, o in zip(U, got):
         _check(u, o)
+
+
+@pytest.mark.parametrize("N,K", [(40, 100), (160, 300), (260, 300)])
+@pytest.mark.parametrize("rows", [
+    [(0.1, 0.0, 0.0)] * 5,                          # bounds down to 2^-14 and 2^-17
+    [(0.01, 0.0, 0.0)] * 3,
+    [(1e-6, 0.0, 0.0), (0.5, -2.0 ** 38, 0.0)],     # a cubic that is felt at 2^-20
+    [(0.001, 0.0, 0.0), (0.0, 1e6, 0.0)],           # and all of the next X
+    [(1e-30, 0.0, 0.0)],                            # the last step may end anywhere
+    [(1e-3, 0.0, 0.0)] * 8,                         # down to 2^-70, then 2^-80
+    [(1e-6, 0.0, 0.0)] * 6 + [(1e6, 0.0, 0.0)] * 5,
+    [(0.0, 0.0, 0.0)] * 2,
+])
+def test_shrinking_coefficients(N, K, rows):
+    """Iterates that get small keep their digits: their scales follow them.
+    (None of these steps multiplies what another one added by more than 3, so
+    2^-12 covers 22 bits; above 192 rows the fp16 roundings again, here of
+    entries relative to the largest.)"""
+    U = _update(1, N, K, "flat")[0]
+    got = tql.bitnet_orthogonalize(U, steps=len(rows), coefficients=rows)
+    e = _exact(U, rows)
+    size = torch.linalg.matrix_norm(e)
+    tol = (2.0 ** -8 + 2.0 ** -12) * size
+    if min(N, K) > 192:
+        def half(t):
+            unit = 2.0 ** -14 * t.abs().max().clamp(min=2.0 ** -300)
+            return (t / unit).half().double() * unit
+        X = U.double() / (torch.linalg.matrix_norm(U.double()) + 1e-7)
+        tol = tol + 2 * torch.linalg.matrix_norm(_steps(X, rows, half) - e)
+    assert torch.linalg.matrix_norm(got.double() - e) <= tol
+    assert tql.bitnet_device_status(reset=False) == (tql.BITNET_OK, 0)
