@@ -727,11 +727,14 @@ def bitnet_bitdelta_forward(x, W_base, signs, alpha, y_dtype=torch.float32, y=No
     return y
 
 
-def _on(device, stream, run):
+def _on(device, stream, run, *tensors):
     """run(handle) on `device` and on `stream` (the device's current one when
     None), handle being the stream's pointer: memory allocated inside belongs
     to the stream the kernels run on, so a buffer freed on return is not
-    handed to another stream's work."""
+    handed to another stream's work.  `tensors` are the caller's, which may
+    belong to another stream: the allocator is told that a given stream uses
+    them, so that one let go of early is not handed out before the kernels have
+    read it.  (The two streams' order is the caller's.)"""
     if stream is None:
         if torch.cuda.current_device() == device.index:
             # (the current stream's pointer without building a Stream object)
@@ -741,7 +744,11 @@ def _on(device, stream, run):
     if stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        return run(_stream(stream))
+        out = run(_stream(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
 
 
 def _need_one_device(first, *ts):
@@ -804,7 +811,7 @@ def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=N
             ws.data_ptr(), ws.numel(), handle))
         return y, z
 
-    return _on(dev, stream, run)
+    return _on(dev, stream, run, x, W, targets, loss, lse, workspace)
 
 
 def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_dW=True, dx=None,
@@ -837,7 +844,7 @@ def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_
             V, K, _address(gx), _address(gW), ws.data_ptr(), ws.numel(), handle))
         return gx, gW
 
-    return _on(dev, stream, run)
+    return _on(dev, stream, run, x, W, targets, lse, dloss, dx, dW, workspace)
 
 
 # Coefficients a, b, c of the quintic step that bitnet_orthogonalize takes by
@@ -882,7 +889,7 @@ def bitnet_orthogonalize(U, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, ep
             handle))
         return O
 
-    return _on(dev, stream, run)
+    return _on(dev, stream, run, U, out, workspace)
 
 
 def _weights_ptr_layout(W, K):

@@ -399,3 +399,36 @@ def test_many_rows_sum_in_short_runs(M, V, K):
     want = exact - z[torch.arange(M, device="cuda"), t]
     assert ((loss - want).abs() <= e + target + 2.0 ** -22 * want).all(), \
         ((loss - want).abs() / e).max()
+
+
+def _busy(stream):
+    """Hold `stream` for some 50 ms."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)
+
+
+@pytest.mark.parametrize("op", ["forward", "backward", "orthogonalize"])
+def test_temporaries_given_to_another_stream(op):
+    """An input that the caller lets go of while the other stream has not come
+    to it yet stays allocated until that stream has read it."""
+    M, V, K = 1024, 2000, 1024
+    x, W, t, d = _inputs(M, V, K, seed=8)
+    want = _run(x, W, t, d)
+    U = W.float()
+    o_want = tql.bitnet_orthogonalize(U)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy(s)
+    if op == "forward":
+        got = tql.bitnet_cross_entropy_forward(x.clone(), W.clone(), t.clone(), stream=s)
+        pairs = [(got[0], want["loss"]), (got[1], want["lse"])]
+    elif op == "backward":
+        got = tql.bitnet_cross_entropy_backward(x.clone(), W.clone(), t.clone(),
+                                                want["lse"].clone(), d.clone(), stream=s)
+        pairs = [(got[0], want["dx"]), (got[1], want["dW"])]
+    else:
+        pairs = [(tql.bitnet_orthogonalize(U.clone(), stream=s), o_want)]
+    # what the allocator hands out now on the current stream is written at once
+    again = [torch.zeros_like(v) for v in (x, W, t, d, U) for _ in range(16)]
+    torch.cuda.synchronize()
+    assert len(again) == 80 and all(torch.equal(a, b) for a, b in pairs)
