@@ -10,6 +10,7 @@ raised.
 """
 import ctypes
 import functools
+import inspect
 import os
 import threading
 
@@ -189,6 +190,41 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _tensors(args):
+    """The tensors among a call's arguments (tiled weights hold one, groups of
+    problems several)."""
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            yield a
+        elif isinstance(a, (TiledWeights, PairTiledWeights)):
+            yield a.data
+        elif isinstance(a, (list, tuple)):
+            yield from _tensors(a)
+
+
+def _on_given_stream(fn):
+    """With stream= given, run fn with it as the current stream: what fn
+    allocates belongs to the stream that the kernels run on, and the allocator
+    knows of that stream's use of the arguments, so no memory that the kernels
+    still read or write is handed out when the call returns.  (The order of the
+    two streams' work is the caller's.)"""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        args = [list(a) if hasattr(a, "__next__") else a for a in args]
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kwargs)
+        for t in _tensors([*args, *kwargs.values()]):
+            t.record_stream(stream)
+        return out
+
+    return call
+
+
 def _dtype_code(dt):
     if dt == torch.float32:
         return BITNET_F32
@@ -287,6 +323,7 @@ def _expect_weights(W):
     return W.shape
 
 
+@_on_given_stream
 def bitnet_quantize_pack_weights(W, W_packed=None, s_w=None, workspace=None, stream=None):
     """W fp32 [N,K] -> (W_packed uint8 [N,K/4], s_w fp32 [1]) on W's device."""
     N, K = _expect_weights(W)
@@ -310,6 +347,7 @@ def bitnet_quantize_pack_weights(W, W_packed=None, s_w=None, workspace=None, str
     return W_packed, s_w
 
 
+@_on_given_stream
 def bitnet_quantize_pack_weights_static(W, W_packed, s_w, stream=None):
     """Weight quantization + packing that allocates nothing: for callers that
     cannot allocate device memory (e.g. plugins of an engine that owns the
@@ -327,6 +365,7 @@ def bitnet_quantize_pack_weights_static(W, W_packed, s_w, stream=None):
     return W_packed, s_w
 
 
+@_on_given_stream
 def bitnet_rmsnorm_quant_act(x, gamma=None, eps=1e-5, x_q=None, s_x=None, stream=None):
     """x [M,K] fp32/bf16 -> (x_q int8 [M,K], s_x fp32 [M])."""
     M, K = _expect_x(x)
@@ -365,6 +404,7 @@ def _expect_scale(s_w):
     _expect(s_w, "s_w", torch.float32, numel=1)
 
 
+@_on_given_stream
 def bitnet_linear_forward(x, gamma, eps, W_packed, s_w, y_dtype=torch.bfloat16, y=None,
                           workspace=None, stream=None):
     """y = BitLinear(x) with packed ternary weights; y [M,N] in y_dtype."""
@@ -387,6 +427,7 @@ def bitnet_linear_forward(x, gamma, eps, W_packed, s_w, y_dtype=torch.bfloat16, 
     return y
 
 
+@_on_given_stream
 def bitnet_linear_quantize_input(x, gamma, eps, N, workspace, stream=None):
     """Phase 1 of the forward: quantize x [M,K] into `workspace` (sized for (M,N,K))."""
     M, K = _expect_x(x)
@@ -400,6 +441,7 @@ def bitnet_linear_quantize_input(x, gamma, eps, N, workspace, stream=None):
     return workspace
 
 
+@_on_given_stream
 def bitnet_linear_matmul(W_packed, s_w, M, K, workspace, y_dtype=torch.bfloat16, y=None,
                          stream=None):
     """Phase 2: y [M,N] = dequant(quantized input in `workspace` x ternary(W)^T)."""
@@ -438,6 +480,7 @@ def bitnet_tiled_weights_bytes(N: int, K: int) -> int:
     return int(load_library().bitnet_tiled_weights_bytes(int(N), int(K)))
 
 
+@_on_given_stream
 def bitnet_tile_weights(W_packed, out=None, stream=None):
     """Row-major packed weights uint8 [N, K/4] -> TiledWeights (same codes,
     in the tiled order the matmul kernels stream fastest)."""
@@ -471,6 +514,7 @@ def bitnet_tiled_pair_weights_bytes(N: int, K: int) -> int:
     return int(load_library().bitnet_tiled_pair_weights_bytes(int(N), int(K)))
 
 
+@_on_given_stream
 def bitnet_tile_weights_pair(W_gate, W_up, out=None, stream=None):
     """Two row-major packed matrices of the same shape [N, K/4] -> their
     pair-tiled layout (for bitnet_swiglu_forward)."""
@@ -492,6 +536,7 @@ def bitnet_tile_weights_pair(W_gate, W_up, out=None, stream=None):
     return PairTiledWeights(out, N, K)
 
 
+@_on_given_stream
 def bitnet_swiglu_forward(x, gamma, eps, W_pair, s_w_gate, s_w_up, y_dtype=torch.bfloat16,
                           y=None, workspace=None, stream=None):
     """silu(gate) * up of the two BitLinear forwards of x (M <= 16 tokens),
@@ -520,6 +565,7 @@ def bitnet_swiglu_forward(x, gamma, eps, W_pair, s_w_gate, s_w_up, y_dtype=torch
     return y
 
 
+@_on_given_stream
 def bitnet_quantize_pack_weights_group_scales(W, group_k, W_packed=None, s_w=None,
                                               workspace=None, stream=None):
     """W fp32 [N,K] -> (W_packed uint8 [N,K/4], s_w fp32 [K/group_k]): one
@@ -551,6 +597,7 @@ def bitnet_quantize_pack_weights_group_scales(W, group_k, W_packed=None, s_w=Non
     return W_packed, s_w
 
 
+@_on_given_stream
 def bitnet_linear_forward_group_scales(x, gamma, eps, W, s_w, group_k, y_dtype=torch.float32,
                                        y=None, debug=False, workspace=None, stream=None):
     """The forward with group-wise scales (W row-major [N, K/4] or
@@ -596,6 +643,7 @@ def _check_lambda(lam):
     return lam
 
 
+@_on_given_stream
 def bitnet_warmup_quantize_weights(W, lam, W_lam=None, s_w=None, workspace=None, stream=None):
     """W fp32 [N,K] -> (W_lam bf16 [N,K], s_w fp32 [1]): the warm-up blend
     W + lam (t / s_w - W) of the weights, rounded to bf16."""
@@ -622,6 +670,7 @@ def bitnet_warmup_quantize_weights(W, lam, W_lam=None, s_w=None, workspace=None,
     return W_lam, s_w
 
 
+@_on_given_stream
 def bitnet_warmup_forward(x, gamma, eps, W_lam, lam, y_dtype=torch.float32, y=None,
                           keep_x_lam=False, stream=None):
     """y = x_lam W_lam^T with x_lam = x_n + lam (x_q / s_x - x_n) (bf16 tensor
@@ -652,6 +701,7 @@ def bitnet_warmup_forward(x, gamma, eps, W_lam, lam, y_dtype=torch.float32, y=No
     return (y, x_lam) if keep_x_lam else y
 
 
+@_on_given_stream
 def bitnet_warmup_backward(dy, x_lam, W_lam, need_dx=True, need_dW=True, stream=None):
     """Straight-through backward of y = x_lam W_lam^T: (dx fp32 [M,K] = dy
     W_lam, dW fp32 [N,K] = dy^T x_lam); either may be skipped (None)."""
@@ -675,6 +725,7 @@ def bitnet_warmup_backward(dy, x_lam, W_lam, need_dx=True, need_dW=True, stream=
     return dx, dW
 
 
+@_on_given_stream
 def bitnet_bitdelta_compress(W_base, W_fine, signs=None, alpha=None, stream=None):
     """W_base, W_fine bf16 [N,K] -> (signs int32 [N, K/32] (the bit patterns of
     the uint32 words), alpha fp32 [1])."""
@@ -704,6 +755,7 @@ def bitnet_bitdelta_compress(W_base, W_fine, signs=None, alpha=None, stream=None
     return signs, alpha
 
 
+@_on_given_stream
 def bitnet_bitdelta_forward(x, W_base, signs, alpha, y_dtype=torch.float32, y=None, stream=None):
     """B <= 8 tenants, one token each: x bf16 [B,K], W_base bf16 [N,K], signs
     int32 [B, N, K/32], alpha fp32 [B] -> y [B,N] = x W_base^T + alpha_b x Sign_b^T."""
@@ -926,6 +978,7 @@ def grouped_problems(items):
     return arr, len(items)
 
 
+@_on_given_stream
 def bitnet_linear_forward_ex(x, gamma, eps, W, s_w, y_dtype=torch.float32, y=None,
                              path=BITNET_PATH_AUTO, want_y=True, debug=True, workspace=None,
                              stream=None):
@@ -968,6 +1021,7 @@ def bitnet_linear_forward_grouped_workspace_bytes(problems, count):
         count, ctypes.cast(problems, ctypes.c_void_p)))
 
 
+@_on_given_stream
 def bitnet_linear_forward_grouped(items, workspace=None, phases=BITNET_PHASE_ALL, stream=None):
     """Run several independent forwards in one call.  items: list of
     (x, gamma, eps, W_packed, s_w, y) with y preallocated [M, N]."""
@@ -984,6 +1038,7 @@ def bitnet_linear_forward_grouped(items, workspace=None, phases=BITNET_PHASE_ALL
     return [it[5] for it in items]
 
 
+@_on_given_stream
 def bitnet_linear_forward_debug(x, gamma, eps, W_packed, s_w, y_dtype=torch.float32,
                                 path=BITNET_PATH_AUTO, want_y=True, workspace=None,
                                 stream=None):
@@ -1010,6 +1065,7 @@ def bitnet_linear_forward_debug(x, gamma, eps, W_packed, s_w, y_dtype=torch.floa
     return {"y": y, "x_q": x_q, "s_x": s_x, "acc": acc}
 
 
+@_on_given_stream
 def bitnet_ternary_matmul_i32(x_q, W_packed, path=BITNET_PATH_AUTO, acc=None, workspace=None,
                               stream=None):
     """acc int32 [M,N] = x_q (int8 [M,K]) times the ternary weights transposed."""
@@ -1054,6 +1110,7 @@ def bitnet_selftest_mma_i8(iters, ctas, a_in_tmem=False, stream=None):
     return 2 * 128 * 256 * 32 * int(iters) * int(ctas)
 
 
+@_on_given_stream
 def bitnet_selftest_divide(a, b, stream=None):
     """a / b (fp32 CUDA tensors) through the decode epilogue's division."""
     _expect(a, "a", torch.float32)
