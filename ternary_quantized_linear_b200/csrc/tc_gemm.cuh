@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
 tc_gemm_kernel(const __grid_constant__ TgMaps maps, const TgShape p,
                const typename Epi::Params ep) {
   using C = TgCfg<CG, BN, Epi>;
-  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 && C::RING_BYTES >= 65536 + ((3 + SPLIT) / SPLIT) * SPLIT * 16384),
+  static_assert(SPLIT == 1 || (CG == 1 && BN == 128 &&
+                               C::RING_BYTES >= 65536 + ((3 + SPLIT) / SPLIT) * SPLIT * 16384),
                 "split");
   extern __shared__ uint8_t tg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(

@@ -117,14 +117,17 @@ double tg_cost(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, con
 }
 
 // Pairs on 256 x 256 tiles, or single SMs on 128 x 128 tiles, each tile's
-// steps shared by a cluster of one of the sizes in `splits` (a bit each):
-// whichever tg_cost prefers.  Every CTA of a cluster needs a step of its own.
+// steps shared by a cluster of up to max_split: whichever tg_cost prefers.
+// Every CTA of a cluster needs a step of its own.  (Only X X^T asks for a split:
+// by two, three or four it pays for the parts' meeting from 25, 19 or 17 steps
+// on, and R R and Q X with as many, n = 1570, 1180 or 1050, have more tiles than
+// clusters are resident.)
 TgPlan tg_plan(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, int passes,
-               unsigned splits) {
+               int max_split = 1) {
   TgPlan best{2, 256, 1};
   double cost = tg_cost(M, N, batch, sym, steps * passes, best);
-  for (int s = 1; s <= 4; ++s) {
-    if (!(splits >> s & 1u) || (s - 1) * ceil_div(steps, s) >= steps) continue;
+  for (int s = 1; s <= max_split; ++s) {
+    if ((s - 1) * ceil_div(steps, s) >= steps) continue;
     const TgPlan pl{1, 128, s};
     const double c = tg_cost(M, N, batch, sym, ceil_div(steps, s) * s * passes, pl);
     if (c < cost) {
@@ -134,8 +137,6 @@ TgPlan tg_plan(int64_t M, int64_t N, int64_t batch, bool sym, int64_t steps, int
   }
   return best;
 }
-constexpr unsigned kNoSplit = 1u << 1, kSplit124 = 1u << 1 | 1u << 2 | 1u << 4,
-                   kSplit1234 = kSplit124 | 1u << 3;
 
 // Resident workers (pairs or single CTAs) of one kernel instance, per device;
 // sets the kernel's shared-memory limit the first time.
@@ -289,20 +290,15 @@ bitnet_status launch_logits(const DeviceState& ds, const TgProblem& g,
   return launch_tg<256, Epi>(ds, g, ep, stream);
 }
 
-// The same with the contraction of a 128 x 128 tile shared by a cluster.
-template <class Epi>
-bitnet_status launch_tg_split(const DeviceState& ds, const TgProblem& g,
-                              const typename Epi::Params& ep, cudaStream_t stream,
-                              TgReady* ready) {
+// X X^T, whose contraction is the long side: a 128 x 128 tile's may be shared by
+// a cluster.
+bitnet_status launch_gram(const DeviceState& ds, const TgProblem& g, const OrthoGram::Params& ep,
+                          cudaStream_t stream, TgReady* ready) {
   switch (g.plan.split) {
-    case 3:
-      // (only X X^T's epilogue leaves the ring room for three parts of two chunks)
-      if constexpr (TgCfg<1, 128, Epi>::RING_BYTES >= 163840)
-        return launch_tg_cfg<1, 128, 3, Epi>(ds, g, ep, stream, ready);
-      return BITNET_ERR_INVALID_ARG;
-    case 2: return launch_tg_cfg<1, 128, 2, Epi>(ds, g, ep, stream, ready);
-    case 4: return launch_tg_cfg<1, 128, 4, Epi>(ds, g, ep, stream, ready);
-    default: return launch_tg<128, Epi>(ds, g, ep, stream, ready);
+    case 2: return launch_tg_cfg<1, 128, 2, OrthoGram>(ds, g, ep, stream, ready);
+    case 3: return launch_tg_cfg<1, 128, 3, OrthoGram>(ds, g, ep, stream, ready);
+    case 4: return launch_tg_cfg<1, 128, 4, OrthoGram>(ds, g, ep, stream, ready);
+    default: return launch_tg<128, OrthoGram>(ds, g, ep, stream, ready);
   }
 }
 
@@ -337,7 +333,7 @@ bitnet_status check_ce_shape(int64_t M, int64_t V, int64_t K) {
 // columns evenly over all of them (a multiple of `unit`).
 TgPlan ce_logits_plan(int64_t M, int64_t cols, int64_t K, int unit) {
   if (M > 128) {
-    const TgPlan pl = tg_plan(M, cols, 1, false, ceil_div(K, kTgKStep), 1, kNoSplit);
+    const TgPlan pl = tg_plan(M, cols, 1, false, ceil_div(K, kTgKStep), 1);
     return pl;
   }
   const int64_t rounds = ceil_div(cols, 256LL * kPlanSms);
@@ -759,7 +755,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.M = cols;
       g.N = K;
       g.Kc = M;
-      g.plan = tg_plan(cols, K, 1, false, ceil_div(M, kTgKStep), 1, kNoSplit);
+      g.plan = tg_plan(cols, K, 1, false, ceil_div(M, kTgKStep), 1);
       st = launch_tg<128, TgStoreBf16>(*ds, g, TgStoreBf16::Params{scale}, s);
       if (st != BITNET_OK) return st;
     }
@@ -840,9 +836,9 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
 
   const int passes = L.split ? 3 : 1;
   const int64_t n_steps = ceil_div(L.n, kTgKStep), k_steps = ceil_div(L.k, kTgKStep);
-  const TgPlan gram_plan = tg_plan(L.n, L.n, B, !L.split, k_steps, passes, kSplit1234);
-  const TgPlan poly_plan = tg_plan(L.n, L.n, B, !L.split, n_steps, passes, kSplit124);
-  const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes, kSplit124);
+  const TgPlan gram_plan = tg_plan(L.n, L.n, B, !L.split, k_steps, passes, 4);
+  const TgPlan poly_plan = tg_plan(L.n, L.n, B, !L.split, n_steps, passes);
+  const TgPlan update_plan = tg_plan(L.n, L.k, B, false, n_steps, passes);
   // The result goes out by TMA where its rows are whole 16-byte pieces.
   const bool direct = !tall && L.k % 8 != 0;
   TgReady gram_ready[2], poly_ready, update_ready[2], last_ready;
@@ -871,7 +867,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.out.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     g.plan = gram_plan;
     OrthoGram::Params gram{D, L.split ? 1 : 0, f};
-    st = launch_tg_split<OrthoGram>(*ds, g, gram, s, &gram_ready[from]);
+    st = launch_gram(*ds, g, gram, s, &gram_ready[from]);
     if (st != BITNET_OK) return st;
     // R R -> Q, E
     g.Kc = L.n;
@@ -885,7 +881,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.out.lo = Q_lo;
     g.plan = poly_plan;
     OrthoPoly::Params poly_p{D, E, L.split ? 1 : 0, f};
-    st = launch_tg_split<OrthoPoly>(*ds, g, poly_p, s, &poly_ready);
+    st = launch_tg<128, OrthoPoly>(*ds, g, poly_p, s, &poly_ready);
     if (st != BITNET_OK) return st;
     // X <- E X + Q X
     g.sym = false;
@@ -915,7 +911,7 @@ BITNET_API bitnet_status bitnet_orthogonalize(const void* U, int u_dtype, int64_
     g.plan = update_plan;
     OrthoUpdate::Params up{E, last ? static_cast<__nv_bfloat16*>(O) : nullptr, tall ? 1 : 0,
                            direct ? 1 : 0, f.ku};
-    st = launch_tg_split<OrthoUpdate>(*ds, g, up, s, last ? &last_ready : &update_ready[from]);
+    st = launch_tg<128, OrthoUpdate>(*ds, g, up, s, last ? &last_ready : &update_ready[from]);
     if (st != BITNET_OK) return st;
   }
   return BITNET_OK;
