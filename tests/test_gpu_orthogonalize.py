@@ -304,3 +304,18 @@ def test_shrinking_coefficients(N, K, rows):
         tol = tol + 2 * torch.linalg.matrix_norm(_steps(X, rows, half) - e)
     assert torch.linalg.matrix_norm(got.double() - e) <= tol
     assert tql.bitnet_device_status(reset=False) == (tql.BITNET_OK, 0)
+
+
+@pytest.mark.parametrize("B,N,K", [
+    (1, 904, 1256), (1, 1256, 905),          # X X^T on clusters of three
+    (1, 1179, 1621), (200, 1, 2054),         # of two
+    (1, 195, 1106), (1, 3, 4100),            # of four
+    (1, 130, 514),                           # of three, both halves
+    (16, 389, 406), (40, 194, 200),          # SM pairs over a stack
+    (40, 137, 137),                          # the same, both halves
+    (8, 512, 1024),                          # single SMs, and pairs for the update
+])
+def test_every_cut_of_the_products(B, N, K):
+    """A shape for each way that the products can be cut."""
+    U = _update(B, N, K, "flat", torch.float32, seed=B + N + K)
+    _check(U, tql.bitnet_orthogonalize(U))
