@@ -432,3 +432,42 @@ def test_temporaries_given_to_another_stream(op):
     again = [torch.zeros_like(v) for v in (x, W, t, d, U) for _ in range(16)]
     torch.cuda.synchronize()
     assert len(again) == 80 and all(torch.equal(a, b) for a, b in pairs)
+
+
+@pytest.mark.parametrize("M,V,K", [(300, 40001, 1544), (1500, 20003, 1032), (129, 45000, 2056)])
+def test_runs_of_pairs_over_several_tiles(M, V, K):
+    """More 256 x 256 tiles than SM pairs, each of more than one run of 1024
+    terms (the last one short): loss and gradient."""
+    x, W, t, d = _inputs(M, V, K, seed=M + V, sigma=0.02)
+    exact, tol = _exact(x, W, t, d)
+    _close(_run(x, W, t, d), exact, tol)
+    assert tql.bitnet_device_status(reset=False) == (tql.BITNET_OK, 0)
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 90001, 64), (1, 5003, 1032), (100, 40001, 64),
+                                   (128, 33000, 72), (200, 21000, 64), (300, 2049, 520)])
+def test_every_edge_column_counts_once(M, V, K):
+    """One entry far above the rest, at either side of every kind of edge (a
+    chunk of 32 columns, a tile of any width, the last column): left out or
+    counted twice it would move lse by ln 2 at least."""
+    g = torch.Generator(device="cuda").manual_seed(M + V)
+    x = torch.randn((M, K), generator=g, device="cuda")
+    x[:, 0] = 1.0
+    x = x.bfloat16()
+    W = (0.01 * torch.randn((V, K), generator=g, device="cuda")).bfloat16()
+    W[:, 0] = 0.0
+    t = torch.full((M,), V // 2 + 1, device="cuda")
+    cols = {0, 1, V - 1, V - 2}
+    for width in range(16, 272, 16):       # tiles are a multiple of 16 columns wide
+        for n in (1, 2, V // width // 2, V // width):
+            cols |= {n * width - 1, n * width}
+    cols |= {c for c in range(0, min(V, 1056))}
+    for c in sorted(c for c in cols if 0 <= c < V and c != V // 2 + 1):
+        old = W[c, 0].clone()
+        W[c, 0] = 30.0                      # e^30 against e^(+-1) of all others
+        _, lse = tql.bitnet_cross_entropy_forward(x, W, t)
+        W[c, 0] = old
+        z = 30.0 + (x[:, 1:].double() @ W[c, 1:].double())
+        # the others' share is below V e^-28; z itself, 30 and some +-10 of small
+        # terms, is within (K/16 + 64) 2^-23 * 40 < 7e-4
+        assert ((lse.double() - z).abs() <= 1e-3).all(), (c, (lse.double() - z).abs().max())
