@@ -813,6 +813,21 @@ def _need_one_device(first, *ts):
     return device
 
 
+def _need_apart(outputs, inputs):
+    """Refuse given output buffers that overlap one another or an input: the
+    kernels read inputs after they have begun to write."""
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+    seen = [span(t) for t in inputs if t.numel()]
+    for name, t in outputs:
+        if t is not None and t.numel():
+            at, end = span(t)
+            if any(at < e and a < end for a, e in seen):
+                raise ValueError(f"{name} overlaps another tensor of the call")
+            seen.append((at, end))
+
+
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name, *sizes):
     return int(getattr(load_library(), name)(*sizes))
@@ -853,6 +868,8 @@ def bitnet_cross_entropy_forward(x, W, targets, loss=None, lse=None, workspace=N
     if workspace is not None:
         _expect(workspace, "workspace", torch.uint8, numel=nb)
     dev = _need_one_device(x, W, targets, loss, lse, workspace)
+    if not (loss is None and lse is None and workspace is None):
+        _need_apart((("loss", loss), ("lse", lse), ("workspace", workspace)), (x, W, targets))
 
     def run(handle):
         y = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
@@ -883,6 +900,9 @@ def bitnet_cross_entropy_backward(x, W, targets, lse, dloss, need_dx=True, need_
     if workspace is not None:
         _expect(workspace, "workspace", torch.uint8, numel=nb)
     dev = _need_one_device(x, W, targets, lse, dloss, dx, dW, workspace)
+    if not (dx is None and dW is None and workspace is None):
+        _need_apart((("dx", dx), ("dW", dW), ("workspace", workspace)),
+                    (x, W, targets, lse, dloss))
 
     def run(handle):
         gx, gW = dx if need_dx else None, dW if need_dW else None
@@ -931,6 +951,8 @@ def bitnet_orthogonalize(U, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, ep
     if workspace is not None:
         _expect(workspace, "workspace", torch.uint8, numel=nb)
     dev = _need_one_device(U, out, workspace)
+    if not (out is None and workspace is None):
+        _need_apart((("out", out), ("workspace", workspace)), (U,))
 
     def run(handle):
         O = torch.empty(tuple(U.shape), dtype=torch.bfloat16, device=dev) if out is None else out

@@ -471,3 +471,28 @@ def test_every_edge_column_counts_once(M, V, K):
         # the others' share is below V e^-28; z itself, 30 and some +-10 of small
         # terms, is within (K/16 + 64) 2^-23 * 40 < 7e-4
         assert ((lse.double() - z).abs() <= 1e-3).all(), (c, (lse.double() - z).abs().max())
+
+
+def test_overlapping_buffers_are_refused():
+    M, V, K = 40, 300, 64
+    x, W, t, d = _inputs(M, V, K)
+    loss, lse = tql.bitnet_cross_entropy_forward(x, W, t)
+    both = torch.empty(M + 1, device="cuda")
+    big = torch.empty(V + M, K, dtype=torch.bfloat16, device="cuda")
+    square = torch.randn(256, 256, device="cuda").bfloat16()
+    scratch = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    for call in (
+            lambda: tql.bitnet_cross_entropy_forward(x, W, t, loss=both[:M], lse=both[1:]),
+            lambda: tql.bitnet_cross_entropy_backward(x, W, t, lse, d, dx=x),
+            lambda: tql.bitnet_cross_entropy_backward(x, W, t, lse, d, dW=W),
+            lambda: tql.bitnet_cross_entropy_backward(x, W, t, lse, d, dx=big[V - 1:V + M - 1],
+                                                      dW=big[:V]),
+            lambda: tql.bitnet_orthogonalize(square, out=square),
+            lambda: tql.bitnet_orthogonalize(scratch[:1 << 16].view(torch.float32).view(128, 128),
+                                             workspace=scratch)):
+        with pytest.raises(ValueError):
+            call()
+    # neighbours do not overlap
+    dx, dW = tql.bitnet_cross_entropy_backward(x, W, t, lse, d, dx=big[V:], dW=big[:V])
+    want = _run(x, W, t, d)
+    assert torch.equal(dx, want["dx"]) and torch.equal(dW, want["dW"])
