@@ -489,7 +489,8 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
  *   dx [M][K], dW [V][K] bf16, either may be NULL (not computed).
  *   All sums and the softmax's maximum, sum and logarithm are fp32; loss is
  *   log(1 + sum over the others of exp(z_v - z_t)), so a confident token's
- *   keeps its digits; g / max|dloss| (over the finite ones of tokens with a
+ *   keeps its digits (its gradient only as many as lse, in fp32, leaves of
+ *   z_t - lse); g / max|dloss| (over the finite ones of tokens with a
  *   target) is rounded to bf16 as an operand of the two gradient products.  A
  *   dloss of inf or NaN makes its own token's dx non-finite, and dW.
  *   A logit of +inf or NaN gives its row a non-finite lse and loss.  One of
@@ -540,9 +541,11 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void *x, const void
  * (BITNET_ERR_INVALID_ARG).
  * Shapes: 1 <= N, K <= BITNET_MAX_K, 0 <= B <= 65535, at most 2^30 tiles of
  * 128 x 128 in all.  U, O 16-byte aligned; workspace >= the size query (0,
- * and NULL allowed, for updates of up to 128 x 2048 or 2048 x 128), 256-byte
+ * and NULL allowed, for updates of up to 128 x 2048 or 2048 x 128, and to 4096
+ * for up to 14 of them), 256-byte
  * aligned, contents on entry irrelevant; one per call in flight.
- * The same input gives the same bits on every call.  As above, the first call
+ * The same input gives the same bits on every call (a matrix in a batch of
+ * another size may be cut differently).  As above, the first call
  * on a device comes before any stream capture there.
  * ---------------------------------------------------------------------- */
 BITNET_API size_t bitnet_orthogonalize_workspace_bytes(int64_t B, int64_t N, int64_t K);

@@ -3,7 +3,9 @@
 Thin ctypes marshalling over libbitnet_b200.so: the functions below carry the
 names of the C entry points declared in include/bitnet_b200.h, take torch
 CUDA tensors, check dtypes/shapes, and pass raw device pointers plus the
-current CUDA stream.  Every step of the computation runs in the library's
+current CUDA stream, or the one given as stream= (results then belong to it; a
+caller who reads them elsewhere, or whose inputs come from elsewhere, orders the
+two streams).  Every step of the computation runs in the library's
 CUDA kernels; PyTorch only provides device memory and streams.  There is no
 CPU fallback: if the library is missing or a call fails, an exception is
 raised.

@@ -14,7 +14,9 @@
 // rounded sums (the tensor cores truncate theirs, which at 4096 terms of one
 // sign makes a logit 1e-5 of itself too small): with s the sum of exp(z_v - z_t) over the
 // others, loss = log(1 + s) has no cancellation for a confident token, and
-// the target's entry of the gradient is exp(z_t - lse) - 1 by expm1.
+// the target's entry of the gradient is exp(z_t - lse) - 1 by expm1.  lse comes
+// back in fp32, so that entry is good to half a unit of lse's last place, 1e-6
+// for logits near 30: a token whose loss is no larger has no better gradient.
 // Backward: the vocabulary is taken in pieces; the same product forms g of a
 // piece (bf16, in the workspace) from the saved lse, and two more give dx
 // (summed over the pieces in fp32) and the piece's rows of dW.
@@ -68,7 +70,7 @@ __device__ __forceinline__ float ce_target_dot(const __nv_bfloat16* __restrict__
 // pairs, where a run has to outlast half of the epilogue (8 there: 8192 tokens
 // over 128000 x 4096 6.35 ms, 16: 6.01).  100 tokens over 2000 x 4096, all
 // terms positive: lse off by 1.4e-5 instead of 4.4e-4, and one token's loss by
-// 1e-7 of itself instead of 1e-6, in the same time (48.5 us over 32000 x 4096);
+// 1e-7 of itself instead of 1e-6, in the same time (51 us over 32000 x 4096);
 // 256 tokens over 40000 x 4096: 4.2e-5 instead of 4.2e-4.  The loss takes the
 // target's logit from a sum of its own, so what the others lose stays in it.
 // CeGrad forms its logits in runs as short (from the other end of the

@@ -16,8 +16,8 @@
 // MMA work; CG = 1 is for outputs with few tiles.  An SM takes 64 bytes a
 // cycle from L2, and a 64-k step of a 256 x 256 pair tile needs 32 KiB per SM
 // and 512 cycles of MMA: both just meet, while a 128 x 128 tile, with as many
-// bytes for half the MMA work, runs at half the rate.  SPLIT = 2 to 4
-// (CG = 1) lets a cluster of CTAs share one tile's contraction: each sums its
+// bytes for half the MMA work, runs at half the rate.  SPLIT = 2 to 4 (CG = 1,
+// X X^T) lets a cluster of CTAs share one tile's contraction: each sums its
 // part, the parts meet through distributed shared memory, added in rank
 // order, and each CTA finishes its share of the columns.
 //
@@ -52,8 +52,10 @@
 // nobody reads, and the ring holds more stages.  Reading a head for one token
 // needs them: a 224 x 64 piece of it takes 3.6 us to arrive when all SMs ask.
 //
-// Every wait is bounded; on a timeout the kernel records the failure, lets
-// its copies land and exits.
+// Every wait on a barrier in shared memory is bounded; on a timeout the kernel
+// records the failure, lets its copies land and exits.  Cluster barriers and
+// the wait for the launch before have no limit of their own: they end because
+// the peers' and that launch's waits do.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -227,8 +227,8 @@ bitnet_status prepare_tg(const DeviceState& ds, const TgProblem& g, TgReady& r) 
   p.ksplit = g.ksplit;
   p.tiles = static_cast<int>(g.batch * p.per_batch * p.ksplit);
   // Tile rows that share a sweep over n: 8, or up to 16 while their rows of A
-  // stay within 32 MiB of L2 (8192 tokens over 128000 x 4096: 8 rows 7.02 ms,
-  // 16 6.79, 32 7.25).  A contraction of up to 128 is all writing: one, whole
+  // stay within 32 MiB of L2 (8192 tokens over 128000 x 4096: 8 rows 6.16 ms,
+  // 16 6.01, 32 6.40).  A contraction of up to 128 is all writing: one, whole
   // rows of the output at a time (dW of 64 tokens over 50021 x 1608, whose rows
   // share lines, 8 % less than with 8; of 300 tokens 1 % more).
   p.group = g.Kc <= 128 ? 1
@@ -412,8 +412,8 @@ constexpr int64_t kOrthoSplitN = 192;
 
 // Updates that run in one launch: on clusters of up to eight CTAs, or of
 // sixteen, of which seven are resident at a time, for two rounds of them at
-// most (128 x 4096: 1 matrix 101 us, as products of their own 181; 7: 105 and
-// 210; 16: 305 and 268).
+// most (128 x 4096: 1 matrix 101 us, as products of their own 183; 7: 104 and
+// 213; 14: 208 and 263; 16: 306 and 272).
 constexpr int64_t kOsWideBatch = 14;
 
 bool ortho_is_small(int64_t B, int64_t N, int64_t K) {
@@ -423,9 +423,9 @@ bool ortho_is_small(int64_t B, int64_t N, int64_t K) {
 }
 
 // CTAs per matrix: one while it holds all columns; else four or eight of 128
-// columns each while the whole batch is resident (128 x 512: 2 CTAs 87 us, 4
-// 72; x 1024: 4 90, 8 76, 16 74; but 40 of the first 91 and 148, 30 of the
-// second 95 and 166); else as few as hold them.
+// columns each while the whole batch is resident (128 x 512: 2 CTAs 89 us, 4
+// 72; x 1024: 4 91, 8 76, 16 75; but 40 of the first 94 and 148, 30 of the
+// second 96 and 166); else as few as hold them.
 int ortho_small_cluster(int64_t B, int64_t k) {
   if (k <= kOsMaxKs) return 1;
   if (k <= 4 * 128 && B <= 33) return 4;
@@ -690,7 +690,7 @@ BITNET_API bitnet_status bitnet_cross_entropy_backward(const void* x, const void
       g.Kc = K;
       g.plan = ce_logits_plan(M, cols, K, 32);
       // The product before left the ends of W's rows in L2 (64 tokens over
-      // 32000 x 2048, loss and gradient: 149 us from the front, 143 from the end).
+      // 32000 x 2048, loss and gradient: 150 us from the front, 145 from the end).
       g.backwards = true;
       CeGrad::Params ep{targets, lse, dloss, logit, scale, V, v0};
       st = launch_logits<CeGrad>(*ds, g, ep, s);
