@@ -491,8 +491,9 @@ BITNET_API bitnet_status bitnet_warmup_backward(const void *dy, const void *x_la
  *   log(1 + sum over the others of exp(z_v - z_t)), so a confident token's
  *   keeps its digits (its gradient only as many as lse, in fp32, leaves of
  *   z_t - lse); g / max|dloss| (over the finite ones of tokens with a
- *   target) is rounded to bf16 as an operand of the two gradient products.  A
- *   dloss of inf or NaN makes its own token's dx non-finite, and dW.
+ *   target) is rounded to bf16 as an operand of the two gradient products, so a
+ *   dloss below 2^-100 of the largest leaves its token fewer digits.  A dloss of
+ *   inf or NaN makes its own token's dx non-finite, and dW.
  *   A logit of +inf or NaN gives its row a non-finite lse and loss.  One of
  *   -inf has no weight; as the target it makes the loss inf, with lse as it is.
  *   M == 0: the forward queues nothing, the backward zeroes dW.

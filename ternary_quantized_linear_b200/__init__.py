@@ -218,6 +218,7 @@ def _on_given_stream(fn):
         if stream is None:
             return fn(*args, **kwargs)
         args = [list(a) if hasattr(a, "__next__") else a for a in args]
+        kwargs = {k: list(a) if hasattr(a, "__next__") else a for k, a in kwargs.items()}
         with torch.cuda.stream(stream):
             out = fn(*args, **kwargs)
         for t in _tensors([*args, *kwargs.values()]):

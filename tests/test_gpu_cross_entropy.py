@@ -496,3 +496,7 @@ def test_overlapping_buffers_are_refused():
     dx, dW = tql.bitnet_cross_entropy_backward(x, W, t, lse, d, dx=big[V:], dW=big[:V])
     want = _run(x, W, t, d)
     assert torch.equal(dx, want["dx"]) and torch.equal(dW, want["dW"])
+
+
+def test_same_bits_in_runs_on_pairs():
+    test_same_bits_on_streams_and_in_graphs(300, 20000, 1032)

@@ -42,6 +42,10 @@ CALLS = {
     "grouped": lambda v, s: tql.bitnet_linear_forward_grouped(
         ((v("x"), None, 1e-5, v("W_packed"), v("s_w"),
           torch.empty(M, N, dtype=torch.bfloat16, device="cuda")) for _ in range(2)), stream=s),
+    "grouped_by_name": lambda v, s: tql.bitnet_linear_forward_grouped(
+        items=((v("x"), None, 1e-5, v("W_packed"), v("s_w"),
+                torch.empty(M, N, dtype=torch.bfloat16, device="cuda")) for _ in range(2)),
+        stream=s),
     "tile": lambda v, s: tql.bitnet_tile_weights(v("W_packed"), None, s),
     "warmup_weights": lambda v, s: tql.bitnet_warmup_quantize_weights(v("W"), 0.5, stream=s),
     "warmup_forward": lambda v, s: tql.bitnet_warmup_forward(v("x"), None, 1e-5, v("base"), 0.5,
