@@ -500,3 +500,8 @@ def test_overlapping_buffers_are_refused():
 
 def test_same_bits_in_runs_on_pairs():
     test_same_bits_on_streams_and_in_graphs(300, 20000, 1032)
+
+
+@pytest.mark.parametrize("M,V,K", SHAPES)
+def test_results_are_finite(M, V, K):
+    assert all(torch.isfinite(v).all() for v in _run(*_inputs(M, V, K, seed=M + V + K)).values())
